@@ -33,6 +33,9 @@ EXPORTED = ["hstu_layer_fwd", "hstu_layer_fwd_workspace_size", "hstu_f1_fwd", "h
             "hstu_selftest_scratch_cache", "hstu_ln_f2_fwd",
             "hstu_candidate_workspace_size", "hstu_candidate_attention_fwd",
             "hstu_candidate_layer_workspace_size", "hstu_candidate_layer_fwd",
+            "hstu_cache_append", "hstu_paged_attention_workspace_size", "hstu_paged_attention_fwd",
+            "hstu_paged_layer_workspace_size", "hstu_paged_layer_fwd",
+            "hstu_cache_evict_workspace_size", "hstu_cache_evict",
             "hstu_stochastic_length_workspace_size", "hstu_stochastic_length", "hstu_gather_rows",
             "hstu_attention_bwd_workspace_size", "hstu_attention_bwd",
             "hstu_layer_bwd_workspace_size", "hstu_layer_bwd", "hstu_layer_pipeline_create",
@@ -47,6 +50,14 @@ class HstuShape(ctypes.Structure):
                 ("num_heads", ctypes.c_int32), ("d_qk", ctypes.c_int32), ("d_v", ctypes.c_int32),
                 ("n_pos_buckets", ctypes.c_int32), ("n_time_buckets", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("ln_eps", ctypes.c_float)]
+
+
+class HstuPagedCache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("timestamps", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p)]
 
 
 class HstuError(RuntimeError):
@@ -66,6 +77,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, I64, I32, F32, S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
     SH = ctypes.POINTER(HstuShape)
+    PC = ctypes.POINTER(HstuPagedCache)
     sig = {
         "hstu_layer_fwd": ([SH, P, P, P, P, P, P, P, P, P, P, P, P, F32, P, P, S, P], ctypes.c_int),
         "hstu_layer_fwd_workspace_size": ([SH], S),
@@ -95,6 +107,15 @@ def _load() -> ctypes.CDLL:
         "hstu_attention_bwd": ([SH, P, P, P, P, P, P, F32, P, P, P, P, P, P, P, S, P], ctypes.c_int),
         "hstu_candidate_layer_fwd": ([SH, P, P, P, I64, I64, P, P, P, P, P, P, P, P, P, P, P, P, F32,
                                       P, P, S, P], ctypes.c_int),
+        "hstu_cache_append": ([PC, I64, I64, P, P, P, P, I64, P, P, P], ctypes.c_int),
+        "hstu_paged_attention_workspace_size": ([SH], S),
+        "hstu_paged_attention_fwd": ([SH, PC, P, P, I64, P, P, P, P, P, P, F32, I32, P, P, S, P],
+                                     ctypes.c_int),
+        "hstu_paged_layer_workspace_size": ([SH], S),
+        "hstu_paged_layer_fwd": ([SH, PC, P, P, I64, P, P, P, P, P, P, P, P, P, P, P, P, F32, I32, P,
+                                  P, S, P], ctypes.c_int),
+        "hstu_cache_evict_workspace_size": ([PC, I64, I64], S),
+        "hstu_cache_evict": ([PC, I64, P, I64, P, P, I64, I64, P, P, S, P], ctypes.c_int),
         "hstu_layer_bwd_workspace_size": ([SH], S),
         "hstu_layer_pipeline_create": ([SH, I32, ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
         "hstu_layer_pipeline_submit": ([P, SH, P, P, P, P, P, P, P, P, P, P, P, P, F32, P],
@@ -298,6 +319,187 @@ def hstu_candidate_layer_fwd(shape: HstuShape, uvqk_hist, hist_offsets, hist_tim
         _ptr(alibi_slopes), float(scale), _ptr(out_cand), _ptr(workspace), workspace.numel(),
         _stream(stream)), "hstu_candidate_layer_fwd")
     return out_cand
+
+
+class PagedCache:
+    """One layer's paged key-value cache (see the C header): the caller's tensors and the struct that
+    names them.  k, v [num_pages, H, page_size, hd]; positions [num_pages, page_size] int32;
+    timestamps [num_pages, page_size] int64; weights [num_pages, H, page_size] fp32; the last three
+    may be None."""
+
+    def __init__(self, k, v, positions=None, timestamps=None, weights=None):
+        if k.dim() != 4 or not k.is_cuda:
+            raise ValueError("k is a CUDA tensor [num_pages, num_heads, page_size, head_dim]")
+        pages, H, ps, hd = k.shape
+        self.k, self.v, self.positions = k, v, positions
+        self.timestamps, self.weights = timestamps, weights
+        self.device = k.device
+        self.num_pages, self.num_heads, self.page_size, self.head_dim = pages, H, ps, hd
+        n = pages * ps
+        self.struct = HstuPagedCache(
+            pages, ps, H, hd, _dtype_code(k), _arg("k", k, k.dtype, n * H * hd, k.device),
+            _arg("v", v, k.dtype, n * H * hd, k.device),
+            _arg("positions", positions, torch.int32, n, k.device),
+            _arg("timestamps", timestamps, torch.int64, n, k.device),
+            _arg("weights", weights, torch.float32, n * H, k.device))
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def allocate(cls, num_pages: int, page_size: int, num_heads: int, head_dim: int,
+                 dtype=torch.bfloat16, device="cuda", positions: bool = True,
+                 timestamps: bool = True, weights: bool = True) -> "PagedCache":
+        """A cache of new, zeroed tensors."""
+        z = lambda shape, dt, wanted=True: torch.zeros(shape, dtype=dt, device=device) if wanted else None  # noqa: E731
+        kv = (num_pages, num_heads, page_size, head_dim)
+        return cls(z(kv, dtype), z(kv, dtype), z((num_pages, page_size), torch.int32, positions),
+                   z((num_pages, page_size), torch.int64, timestamps),
+                   z((num_pages, num_heads, page_size), torch.float32, weights))
+
+
+def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, device):
+    """Address of a tensor argument of the paged cache's calls, checked; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of {numel} elements on {device} is "
+                         f"wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class _on:
+    """Makes `device` current for a call (kernels launch on the current device)."""
+
+    def __init__(self, device):
+        self._d, self._back = device.index, -1
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if now != self._d:
+            torch.cuda.set_device(self._d)
+            self._back = now
+
+    def __exit__(self, *exc):
+        if self._back >= 0:
+            torch.cuda.set_device(self._back)
+
+
+def _table(cache: PagedCache, page_table, cache_lens, next_positions):
+    if page_table.dim() != 2:
+        raise ValueError("page_table is [num_seqs, max_pages]")
+    B, M = page_table.shape
+    dev = cache.device
+    return B, M, (_arg("page_table", page_table, torch.int32, B * M, dev),
+                  _arg("cache_lens", cache_lens, torch.int64, B, dev),
+                  _arg("next_positions", next_positions, torch.int64, B, dev))
+
+
+def _space(workspace, size, device):
+    """The workspace to use: the caller's (any contiguous tensor on the device) or a new one."""
+    if workspace is None:
+        return torch.empty(max(256, size()), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on {device} is wanted")
+    return workspace
+
+
+def _biases(shape: HstuShape, pos_table, time_table, alibi_slopes, device):
+    H, f = shape.num_heads, torch.float32
+    return (_arg("pos_table", pos_table, f, H * shape.n_pos_buckets, device),
+            _arg("time_table", time_table, f, H * shape.n_time_buckets, device),
+            _arg("alibi_slopes", alibi_slopes, f, H, device))
+
+
+def hstu_cache_append(cache: PagedCache, uvqk, seq_offsets, timestamps, page_table, cache_lens,
+                      next_positions=None, stream=None) -> None:
+    """The K and V rows of a jagged U|V|Q|K batch into the cache (see the C header); cache_lens is
+    the caller's to advance."""
+    B, M, (tp, lp, np_) = _table(cache, page_table, cache_lens, next_positions)
+    n1, dev = 4 * cache.num_heads * cache.head_dim, cache.device
+    T = int(uvqk.shape[0])
+    up = _arg("uvqk", uvqk, cache.k.dtype, T * n1, dev)
+    op = _arg("seq_offsets", seq_offsets, torch.int64, B + 1, dev)
+    sp = _arg("timestamps", timestamps, torch.int64, T, dev)
+    with _on(dev):
+        _check(_lib.hstu_cache_append(cache.ref, B, T, up, op, sp, tp, M, lp, np_,
+                                      _stream(stream)), "hstu_cache_append")
+
+
+def paged_attention_workspace_size(shape: HstuShape) -> int:
+    return int(_lib.hstu_paged_attention_workspace_size(ctypes.byref(shape)))
+
+
+def hstu_paged_attention_fwd(shape: HstuShape, cache: PagedCache, uvqk, page_table, cache_lens,
+                             next_positions, timestamps, pos_table, time_table, alibi_slopes,
+                             scale: float, av, append: bool = True, workspace=None, stream=None):
+    """Attention of one new token a sequence over its cached tokens and itself (see the C header);
+    with `append` the token joins the cache.  Fills and returns av [B, H*hd] (fp32)."""
+    B, M, (tp, lp, np_) = _table(cache, page_table, cache_lens, next_positions)
+    w, dev = cache.num_heads * cache.head_dim, cache.device
+    if shape.num_seqs != B:
+        raise ValueError(f"page_table has {B} rows, the shape {shape.num_seqs} sequences")
+    up = _arg("uvqk", uvqk, cache.k.dtype, B * 4 * w, dev)
+    sp = _arg("timestamps", timestamps, torch.int64, B, dev)
+    ap = _arg("av", av, torch.float32, B * w, dev)
+    pos, tim, ali = _biases(shape, pos_table, time_table, alibi_slopes, dev)
+    ws = _space(workspace, lambda: paged_attention_workspace_size(shape), dev)
+    with _on(dev):
+        _check(_lib.hstu_paged_attention_fwd(
+            ctypes.byref(shape), cache.ref, up, tp, M, lp, np_, sp, pos, tim, ali, scale,
+            1 if append else 0, ap, ws.data_ptr(), ws.nbytes, _stream(stream)),
+            "hstu_paged_attention_fwd")
+    return av
+
+
+def paged_layer_workspace_size(shape: HstuShape) -> int:
+    return int(_lib.hstu_paged_layer_workspace_size(ctypes.byref(shape)))
+
+
+def hstu_paged_layer_fwd(shape: HstuShape, cache: PagedCache, X, page_table, cache_lens,
+                         next_positions, timestamps, W1, b1, W2, b2, ln_w, ln_b, pos_table,
+                         time_table, alibi_slopes, scale: float, out=None, append: bool = True,
+                         workspace=None, stream=None):
+    """One HSTU layer over one new token a sequence, against the layer's paged cache."""
+    B, M, (tp, lp, np_) = _table(cache, page_table, cache_lens, next_positions)
+    w, d, dt, dev = cache.num_heads * cache.head_dim, shape.d_model, cache.k.dtype, cache.device
+    if shape.num_seqs != B:
+        raise ValueError(f"page_table has {B} rows, the shape {shape.num_seqs} sequences")
+    if out is None:
+        out = torch.empty_like(X)
+    args = [_arg("X", X, dt, B * d, dev)]
+    weights = [_arg("W1", W1, dt, d * 4 * w, dev), _arg("b1", b1, dt, 4 * w, dev),
+               _arg("W2", W2, dt, w * d, dev), _arg("b2", b2, dt, d, dev),
+               _arg("ln_w", ln_w, dt, w, dev), _arg("ln_b", ln_b, dt, w, dev)]
+    sp = _arg("timestamps", timestamps, torch.int64, B, dev)
+    pos, tim, ali = _biases(shape, pos_table, time_table, alibi_slopes, dev)
+    op = _arg("out", out, dt, B * d, dev)
+    ws = _space(workspace, lambda: paged_layer_workspace_size(shape), dev)
+    with _on(dev):
+        _check(_lib.hstu_paged_layer_fwd(
+            ctypes.byref(shape), cache.ref, *args, tp, M, lp, np_, sp, *weights, pos, tim, ali,
+            float(scale), 1 if append else 0, op, ws.data_ptr(), ws.nbytes, _stream(stream)),
+            "hstu_paged_layer_fwd")
+    return out
+
+
+def cache_evict_workspace_size(cache: PagedCache, num_seqs: int, max_pages: int) -> int:
+    return int(_lib.hstu_cache_evict_workspace_size(cache.ref, int(num_seqs), int(max_pages)))
+
+
+def hstu_cache_evict(cache: PagedCache, page_table, cache_lens, next_positions, budget: int,
+                     recent: int, new_lens=None, workspace=None, stream=None):
+    """Cuts sequences above `budget` cached tokens to their `recent` newest and the most attended of
+    the others (see the C header).  Returns new_lens [B] (cache_lens itself is allowed)."""
+    B, M, (tp, lp, np_) = _table(cache, page_table, cache_lens, next_positions)
+    dev = cache.device
+    if new_lens is None:
+        new_lens = torch.empty_like(cache_lens)
+    ep = _arg("new_lens", new_lens, torch.int64, B, dev)
+    ws = _space(workspace, lambda: cache_evict_workspace_size(cache, B, M), dev)
+    with _on(dev):
+        _check(_lib.hstu_cache_evict(cache.ref, B, tp, M, lp, np_, budget, recent, ep,
+                                     ws.data_ptr(), ws.nbytes, _stream(stream)),
+               "hstu_cache_evict")
+    return new_lens
 
 
 def hstu_attention_bwd(shape: HstuShape, uvqk, seq_offsets, timestamps, pos_table, time_table,

@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "hbm_kernels.cuh"
 #include "bwd_kernels.cuh"
+#include "paged_kernels.cuh"
 #include "sl_kernels.cuh"
 #include "simt_kernels.cuh"
 #include "tc_kernels.cuh"
@@ -343,6 +344,145 @@ CandWorkspace cand_layout(const hstu_shape_t& s, int64_t Tc, void* base) {
   w.attn = b ? b + o : nullptr;
   w.attn_bytes = tc::candidate_workspace_bytes(Tc, s.num_seqs, s.num_heads);
   o += align_up(w.attn_bytes);
+  w.total = o;
+  return w;
+}
+
+// Paged cache: checks of the struct itself.
+hstu_status_t check_cache(const hstu_paged_cache_t* c) {
+  if (!c) return HSTU_ERR_INVALID_ARG;
+  if (c->num_pages <= 0 || c->num_pages >= (1LL << 31) || c->num_heads <= 0 || c->head_dim <= 0)
+    return HSTU_ERR_INVALID_ARG;
+  if (c->dtype != HSTU_F32 && c->dtype != HSTU_BF16) return HSTU_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+    return HSTU_ERR_INVALID_ARG;
+  if (!paged::head_dim_supported(c->dtype, c->head_dim)) return HSTU_ERR_UNSUPPORTED;
+  if (4LL * c->num_heads * c->head_dim > (1LL << 30)) return HSTU_ERR_INVALID_ARG;
+  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return HSTU_ERR_INVALID_ARG;
+  return HSTU_OK;
+}
+
+size_t cache_bytes(const hstu_paged_cache_t& c) {   // of K, and of V
+  return (size_t)c.num_pages * c.page_size * c.num_heads * c.head_dim * (c.dtype == HSTU_BF16 ? 2 : 4);
+}
+
+// Does [p, p + n) overlap any array of the cache?
+bool overlaps_cache(const void* p, size_t n, const hstu_paged_cache_t& c) {
+  const size_t kv = cache_bytes(c), slots = (size_t)c.num_pages * c.page_size;
+  return overlaps(p, n, c.k, kv) || overlaps(p, n, c.v, kv) ||
+         overlaps(p, n, c.positions, slots * sizeof(int32_t)) ||
+         overlaps(p, n, c.timestamps, slots * sizeof(int64_t)) ||
+         overlaps(p, n, c.weights, slots * c.num_heads * sizeof(float));
+}
+
+paged::Cache cache_view(const hstu_paged_cache_t& c) {
+  int shift = 0;
+  while ((1 << shift) < c.page_size) shift++;
+  return {c.k, c.v, c.positions, c.timestamps, c.weights, c.num_pages, shift, c.num_heads};
+}
+
+hstu_status_t check_table(int64_t num_seqs, const int32_t* page_table, int64_t max_pages,
+                          const int64_t* cache_lens) {
+  if (num_seqs < 0 || max_pages < 0 || max_pages >= (1LL << 31)) return HSTU_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!page_table || !cache_lens || max_pages == 0)) return HSTU_ERR_INVALID_ARG;
+  return HSTU_OK;
+}
+
+// Checks of hstu_paged_attention_fwd's arguments (also used by the paged layer).
+hstu_status_t check_paged(const hstu_shape_t* shape, const hstu_paged_cache_t* cache,
+                          const int32_t* page_table, int64_t max_pages, const int64_t* cache_lens,
+                          const int64_t* timestamps, const float* pos, const float* tim,
+                          const float* alibi, float scale, int32_t append) {
+  hstu_status_t rc = check_shape(shape);
+  if (rc != HSTU_OK) return rc;
+  const hstu_shape_t& s = *shape;
+  if (s.total_tokens != s.num_seqs) return HSTU_ERR_INVALID_ARG;
+  if (s.num_seqs == 0) return HSTU_OK;
+  if ((rc = check_cache(cache)) != HSTU_OK) return rc;
+  if (cache->num_heads != s.num_heads || cache->head_dim != s.d_qk || cache->head_dim != s.d_v ||
+      cache->dtype != s.dtype || s.max_seq_len < 1)
+    return HSTU_ERR_INVALID_ARG;
+  if (s.num_seqs * (int64_t)s.num_heads >= (1LL << 31)) return HSTU_ERR_UNSUPPORTED;
+  if ((rc = check_table(s.num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
+  if ((rc = check_bias(shape, timestamps, pos, tim, alibi, scale)) != HSTU_OK) return rc;
+  if (tim && !cache->timestamps) return HSTU_ERR_INVALID_ARG;
+  if (append && cache->timestamps && !timestamps) return HSTU_ERR_INVALID_ARG;
+  return HSTU_OK;
+}
+
+hstu_status_t run_paged_attention(const hstu_shape_t& s, const hstu_paged_cache_t& cache,
+                                  const void* uvqk, const int32_t* page_table, int64_t max_pages,
+                                  const int64_t* cache_lens, const int64_t* next_positions,
+                                  const int64_t* timestamps, const float* pos, const float* tim,
+                                  const float* alibi, float scale, int32_t append, void* av,
+                                  void* ws, cudaStream_t st) {
+  paged::Attn a{};
+  a.c = cache_view(cache);
+  a.uvqk = uvqk;
+  a.table = page_table;
+  a.max_pages = max_pages;
+  a.lens = cache_lens;
+  a.next_pos = next_positions;
+  a.now = timestamps;
+  a.pos = pos;
+  a.tim = tim;
+  a.alibi = alibi;
+  a.P = s.n_pos_buckets;
+  a.Tb = s.n_time_buckets;
+  a.scale = scale;
+  a.append = append != 0;
+  a.B = s.num_seqs;
+  a.max_len = s.max_seq_len - 1;
+  a.av = (float*)av;
+  (void)ws;
+  return paged::launch_attention(a, s.dtype, s.d_qk, st);
+}
+
+struct PagedWorkspace {
+  void *uvqk, *av, *g, *attn;
+  size_t attn_bytes, total;
+};
+
+PagedWorkspace paged_layout(const hstu_shape_t& s, void* base) {
+  PagedWorkspace w{};
+  const size_t T = (size_t)s.num_seqs, es = esize(s);
+  size_t o = 0;
+  char* b = static_cast<char*>(base);
+  w.uvqk = b ? b + o : nullptr;
+  o += align_up(T * (size_t)n1_of(s) * es);
+  w.av = b ? b + o : nullptr;
+  o += align_up(T * (size_t)wv_of(s) * 4);
+  w.g = b ? b + o : nullptr;
+  o += align_up(T * (size_t)wv_of(s) * es);
+  w.attn = b ? b + o : nullptr;
+  w.attn_bytes = hstu_paged_attention_workspace_size(&s);
+  o += align_up(w.attn_bytes);
+  w.total = o;
+  return w;
+}
+
+struct EvictWorkspace {
+  uint32_t* keys;
+  int64_t *to, *from, *count;
+  int64_t moves;
+  size_t total;
+};
+
+// `room`: slots of a page-table row.  A sequence moves at most min(budget, n - budget) <= room / 2
+// tokens.
+EvictWorkspace evict_layout(int64_t B, int64_t room, void* base) {
+  EvictWorkspace w{};
+  w.moves = room / 2 + 1;
+  size_t o = 0;
+  char* b = static_cast<char*>(base);
+  w.keys = b ? reinterpret_cast<uint32_t*>(b + o) : nullptr;
+  o += align_up((size_t)B * room * sizeof(uint32_t));
+  w.to = b ? reinterpret_cast<int64_t*>(b + o) : nullptr;
+  o += align_up((size_t)B * w.moves * sizeof(int64_t));
+  w.from = b ? reinterpret_cast<int64_t*>(b + o) : nullptr;
+  o += align_up((size_t)B * w.moves * sizeof(int64_t));
+  w.count = b ? reinterpret_cast<int64_t*>(b + o) : nullptr;
+  o += align_up((size_t)B * sizeof(int64_t));
   w.total = o;
   return w;
 }
@@ -913,6 +1053,154 @@ hstu_status_t hstu_layer_bwd(const hstu_shape_t* shape, const void* X, const int
     return rc;
   return tc::launch_gemm_ext<tc::EPI_BIAS_RESIDUAL>(T, d, (int)n1, dz, (const bf16*)w.w1t,
                                                     nullptr, dy, (bf16*)dX, nullptr, 1, -1, st);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Paged cache
+// ------------------------------------------------------------------------------------------------
+
+hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seqs,
+                                int64_t total_tokens, const void* uvqk, const int64_t* seq_offsets,
+                                const int64_t* timestamps, const int32_t* page_table,
+                                int64_t max_pages, const int64_t* cache_lens,
+                                const int64_t* next_positions, void* stream) {
+  hstu_status_t rc = check_cache(cache);
+  if (rc != HSTU_OK) return rc;
+  if (total_tokens < 0 || total_tokens > (1LL << 40)) return HSTU_ERR_INVALID_ARG;
+  if ((rc = check_table(num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
+  if (total_tokens == 0) return HSTU_OK;
+  if (num_seqs == 0 || !uvqk || !seq_offsets || !aligned16(uvqk)) return HSTU_ERR_INVALID_ARG;
+  if (cache->timestamps && !timestamps) return HSTU_ERR_INVALID_ARG;
+  const size_t row = (size_t)4 * cache->num_heads * cache->head_dim * (cache->dtype == HSTU_BF16 ? 2 : 4);
+  if (overlaps_cache(uvqk, (size_t)total_tokens * row, *cache)) return HSTU_ERR_INVALID_ARG;
+  if (total_tokens * cache->num_heads / 8 >= (1LL << 31) - 1) return HSTU_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  check_offsets_kernel<<<(unsigned)((num_seqs + 1 + 255) / 256), 256, 0, st>>>(seq_offsets, num_seqs,
+                                                                              total_tokens);
+  if (launch_status() != HSTU_OK) return HSTU_ERR_CUDA;
+  return paged::launch_append(cache_view(*cache), cache->dtype, cache->head_dim, total_tokens,
+                              num_seqs, uvqk, seq_offsets, timestamps, page_table, max_pages,
+                              cache_lens, next_positions, st);
+}
+
+size_t hstu_paged_attention_workspace_size(const hstu_shape_t* shape) {
+  if (check_shape(shape) != HSTU_OK) return 0;
+  return 0;
+}
+
+hstu_status_t hstu_paged_attention_fwd(const hstu_shape_t* shape, const hstu_paged_cache_t* cache,
+                                       const void* uvqk, const int32_t* page_table,
+                                       int64_t max_pages, const int64_t* cache_lens,
+                                       const int64_t* next_positions, const int64_t* timestamps,
+                                       const float* pos_table, const float* time_table,
+                                       const float* alibi_slopes, float scale, int32_t append,
+                                       void* av, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  hstu_status_t rc = check_paged(shape, cache, page_table, max_pages, cache_lens, timestamps,
+                                 pos_table, time_table, alibi_slopes, scale, append);
+  if (rc != HSTU_OK || shape->num_seqs == 0) return rc;
+  const hstu_shape_t& s = *shape;
+  if (!uvqk || !av || !workspace) return HSTU_ERR_INVALID_ARG;
+  if (!aligned16(uvqk) || !aligned16(av)) return HSTU_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) return HSTU_ERR_INVALID_ARG;
+  if (workspace_bytes < hstu_paged_attention_workspace_size(shape)) return HSTU_ERR_INVALID_ARG;
+  const size_t avb = (size_t)s.num_seqs * wv_of(s) * 4, ub = (size_t)s.num_seqs * n1_of(s) * esize(s);
+  if (overlaps(av, avb, uvqk, ub) || overlaps(av, avb, workspace, workspace_bytes) ||
+      overlaps(uvqk, ub, workspace, workspace_bytes) || overlaps_cache(av, avb, *cache) ||
+      overlaps_cache(uvqk, ub, *cache) || overlaps_cache(workspace, workspace_bytes, *cache))
+    return HSTU_ERR_INVALID_ARG;
+  return run_paged_attention(s, *cache, uvqk, page_table, max_pages, cache_lens, next_positions,
+                             timestamps, pos_table, time_table, alibi_slopes, scale, append, av,
+                             workspace, static_cast<cudaStream_t>(stream));
+}
+
+size_t hstu_paged_layer_workspace_size(const hstu_shape_t* shape) {
+  if (check_shape(shape) != HSTU_OK) return 0;
+  return paged_layout(*shape, nullptr).total;
+}
+
+hstu_status_t hstu_paged_layer_fwd(const hstu_shape_t* shape, const hstu_paged_cache_t* cache,
+                                   const void* X, const int32_t* page_table, int64_t max_pages,
+                                   const int64_t* cache_lens, const int64_t* next_positions,
+                                   const int64_t* timestamps, const void* W1, const void* b1,
+                                   const void* W2, const void* b2, const void* ln_w,
+                                   const void* ln_b, const float* pos_table,
+                                   const float* time_table, const float* alibi_slopes, float scale,
+                                   int32_t append, void* out, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  hstu_status_t rc = check_paged(shape, cache, page_table, max_pages, cache_lens, timestamps,
+                                 pos_table, time_table, alibi_slopes, scale, append);
+  if (rc != HSTU_OK || shape->num_seqs == 0) return rc;
+  const hstu_shape_t& s = *shape;
+  if (!X || !W1 || !W2 || !ln_w || !ln_b || !out || !workspace) return HSTU_ERR_INVALID_ARG;
+  if (s.dtype == HSTU_BF16 && !(aligned16(X) && aligned16(W1) && aligned16(b1) && aligned16(W2) &&
+                                aligned16(b2) && aligned16(ln_w) && aligned16(ln_b) && aligned16(out)))
+    return HSTU_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) return HSTU_ERR_INVALID_ARG;
+  const PagedWorkspace w = paged_layout(s, workspace);
+  if (workspace_bytes < w.total) return HSTU_ERR_INVALID_ARG;
+  const size_t xbytes = (size_t)s.num_seqs * s.d_model * esize(s);
+  if (overlaps(out, xbytes, X, xbytes) || overlaps(out, xbytes, workspace, w.total) ||
+      overlaps(X, xbytes, workspace, w.total) || overlaps_cache(out, xbytes, *cache) ||
+      overlaps_cache(X, xbytes, *cache) || overlaps_cache(workspace, w.total, *cache))
+    return HSTU_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((rc = run_f1(s, X, W1, b1, w.uvqk, st)) != HSTU_OK) return rc;
+  if ((rc = run_paged_attention(s, *cache, w.uvqk, page_table, max_pages, cache_lens, next_positions,
+                                timestamps, pos_table, time_table, alibi_slopes, scale, append,
+                                w.av, w.attn, st)) != HSTU_OK)
+    return rc;
+  if (ln_f2_preferred(s)) return run_ln_f2(s, w.av, w.uvqk, ln_w, ln_b, W2, b2, X, out, st);
+  if ((rc = run_ln_gate(s, w.av, w.uvqk, ln_w, ln_b, w.g, st)) != HSTU_OK) return rc;
+  return run_f2(s, w.g, W2, b2, X, out, st);
+}
+
+size_t hstu_cache_evict_workspace_size(const hstu_paged_cache_t* cache, int64_t num_seqs,
+                                       int64_t max_pages) {
+  if (check_cache(cache) != HSTU_OK || num_seqs < 0 || max_pages < 0 || max_pages >= (1LL << 31))
+    return 0;
+  return evict_layout(num_seqs, max_pages * cache->page_size, nullptr).total;
+}
+
+hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs,
+                               const int32_t* page_table, int64_t max_pages,
+                               const int64_t* cache_lens, const int64_t* next_positions,
+                               int64_t budget, int64_t recent, int64_t* new_lens, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  hstu_status_t rc = check_cache(cache);
+  if (rc != HSTU_OK) return rc;
+  if (budget < 0 || recent < 0 || recent > budget) return HSTU_ERR_INVALID_ARG;
+  if (!cache->positions || !cache->weights) return HSTU_ERR_INVALID_ARG;
+  if ((rc = check_table(num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
+  if (num_seqs == 0) return HSTU_OK;
+  if (num_seqs > 65535) return HSTU_ERR_UNSUPPORTED;
+  if (!new_lens || !workspace) return HSTU_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) return HSTU_ERR_INVALID_ARG;
+  const int64_t room = max_pages * cache->page_size;
+  const EvictWorkspace w = evict_layout(num_seqs, room, workspace);
+  if (workspace_bytes < w.total) return HSTU_ERR_INVALID_ARG;
+  const size_t lb = (size_t)num_seqs * sizeof(int64_t);
+  if ((new_lens != cache_lens && overlaps(new_lens, lb, cache_lens, lb)) ||
+      overlaps(new_lens, lb, next_positions, lb) || overlaps(new_lens, lb, workspace, w.total) ||
+      overlaps_cache(new_lens, lb, *cache) || overlaps_cache(workspace, w.total, *cache))
+    return HSTU_ERR_INVALID_ARG;
+  paged::Evict a{};
+  a.c = cache_view(*cache);
+  a.table = page_table;
+  a.max_pages = max_pages;
+  a.B = num_seqs;
+  a.lens = cache_lens;
+  a.next_pos = next_positions;
+  a.budget = budget;
+  a.recent = recent;
+  a.new_lens = new_lens;
+  a.keys = w.keys;
+  a.to = w.to;
+  a.from = w.from;
+  a.count = w.count;
+  a.room = room;
+  a.moves = w.moves;
+  return paged::launch_evict(a, cache->dtype, cache->head_dim, static_cast<cudaStream_t>(stream));
 }
 
 size_t hstu_stochastic_length_workspace_size(int64_t num_seqs) {

@@ -1,7 +1,8 @@
 /*
  * hstu.h -- C ABI of the B200 (sm_100a) HSTU layer library, libhstu_b200.so: the layer forward,
- * its steps one at a time, M-FALCON candidate scoring, Stochastic Length subsampling, the attention
- * and layer backward passes (training), and a host-to-host forward pipeline.
+ * its steps one at a time, M-FALCON candidate scoring, a paged key-value cache (one new token at a
+ * time, with eviction), Stochastic Length subsampling, the attention and layer backward passes
+ * (training), and a host-to-host forward pipeline.
  *
  * The layer (one "HSTU" block of "Actions Speak Louder than Words", paper notes, section 3.1,
  * Eqs. 1-3; also the HSTU-layer section of "4.4 推荐模型的 Scaling") over a jagged batch of
@@ -338,6 +339,149 @@ hstu_status_t hstu_candidate_layer_fwd(const hstu_shape_t* shape, const void* uv
                                        const float* time_table, const float* alibi_slopes,
                                        float scale, void* out_cand, void* workspace,
                                        size_t workspace_bytes, void* stream);
+
+/*
+ * Paged cache: a layer's history kept in pages, one new token at a time.
+ *
+ * hstu_candidate_attention_fwd scores candidates against the U|V|Q|K of one forward over the whole
+ * history ("Actions Speak Louder than Words" paper notes, section 3.6, the encoder-level K/V
+ * cache).  Here the cache grows: a history's K and V are filled in once (hstu_cache_append), each
+ * new action attends to it and joins it (hstu_paged_attention_fwd, hstu_paged_layer_fwd), and when
+ * it exceeds a budget the tokens that received the least attention leave it (hstu_cache_evict).
+ * The pages describe the cache's reuse, not its paging or eviction.
+ *
+ * One cache holds one layer's K and V for many sequences.  A sequence b with n = cache_lens[b]
+ * cached tokens has them in slots 0 .. n-1; slot i lives in page page_table[b][i / page_size] at
+ * offset i % page_size.  Pages are handed out by the caller; their order is free, and a sequence's
+ * table entries beyond its own tokens are not read.  A negative cache_lens[b] marks an inactive
+ * row of a padded batch.
+ *
+ *  num_pages     pages in the pool, below 2^31
+ *  page_size     tokens a page: a power of two, 16 .. 1024
+ *  num_heads, head_dim (= d_qk = d_v), dtype   as the layer's; bf16: head_dim 64 or 128, fp32: 32,
+ *                64 or 128 (else HSTU_ERR_UNSUPPORTED)
+ *  k, v          [num_pages, num_heads, page_size, head_dim] (dtype), 16-byte aligned
+ *  positions     [num_pages, page_size] int32: the token's position in its history, or NULL (slot i
+ *                holds position i; such a cache cannot evict)
+ *  timestamps    [num_pages, page_size] int64 seconds, or NULL (no time table)
+ *  weights       [num_pages, num_heads, page_size] fp32: sums of |a| that the token received from
+ *                the tokens after it, a head; or NULL (not kept; such a cache cannot evict)
+ * The caller owns every array; the struct is read during the call only.
+ *
+ * Two sequences of one call may share a page that neither call writes: a shared prefix can be read
+ * by hstu_paged_attention_fwd on a cache without weights; pages that are appended to, evicted from
+ * or whose weights are summed belong to one sequence.  Problems only the device sees (a length
+ * beyond the table or max_seq_len, an entry that is no page) are reported as
+ * HSTU_ERR_DEVICE_BAD_OFFSETS: the length is clamped and the tokens of such a page are left out.
+ * Calls that write one cache are ordered by the caller (one stream, or events).
+ */
+typedef struct {
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t num_heads;
+  int32_t head_dim;
+  int32_t dtype;
+  void* k;
+  void* v;
+  int32_t* positions;
+  int64_t* timestamps;
+  float* weights;
+} hstu_paged_cache_t;
+
+/*
+ * hstu_cache_append -- the K and V rows of a jagged U|V|Q|K batch (hstu_f1_fwd's output, a
+ * forward's workspace) into the cache: token i of sequence b goes to slot cache_lens[b] + i, at
+ * position next_positions[b] + i, with its timestamp and zero weights.  cache_lens is not changed:
+ * the caller adds the counts.
+ *
+ *  uvqk           [total_tokens, 4*H*hd] (the cache's dtype), 16-byte aligned
+ *  seq_offsets    [num_seqs + 1] int64, as in hstu_layer_fwd (empty sequences allowed)
+ *  timestamps     [total_tokens] int64, or NULL (required when the cache has timestamps)
+ *  page_table     [num_seqs, max_pages] int32
+ *  cache_lens     [num_seqs] int64
+ *  next_positions [num_seqs] int64, the position of the next token (tokens seen so far, evicted ones
+ *                 included; below 2^31), or NULL: cache_lens
+ * Tokens that do not fit the sequence's pages, or that belong to an inactive sequence, are left
+ * out and reported.  Asynchronous on `stream`.
+ */
+hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seqs,
+                                int64_t total_tokens, const void* uvqk, const int64_t* seq_offsets,
+                                const int64_t* timestamps, const int32_t* page_table,
+                                int64_t max_pages, const int64_t* cache_lens,
+                                const int64_t* next_positions, void* stream);
+
+/*
+ * hstu_paged_attention_fwd -- Eq. 2 for one new token a sequence over its cached tokens and itself:
+ *   x_j = q.k_j + bias(p - p_j, t - t_j),  a_j = scale * SiLU(x_j),
+ *   AV  = sum_{j<n} a_j v_j + scale * SiLU(q.k + bias(0, 0)) v
+ * with p = next_positions[b], t = timestamps[b] and the biases of hstu_layer_fwd (position index
+ * min(max(p - p_j, 0), P - 1); ALiBi -m_h max(p - p_j, 0)).  Without evictions that is the causal
+ * row n of the sequence's forward.
+ *
+ *  shape          num_seqs = total_tokens = B (one token a sequence); max_seq_len >= the longest
+ *                 cached length + 1; heads, head size, dtype as the cache's; tables as usual
+ *  uvqk           [B, 4*H*hd], the new tokens' f1 output (dtype); Q, K and V are read
+ *  page_table     [B, max_pages] int32       cache_lens [B] int64
+ *  next_positions [B] int64 or NULL: cache_lens        timestamps [B] int64 (NULL without time_table
+ *                 unless append is set and the cache has timestamps)
+ *  append         nonzero: the new token's K, V, position, timestamp and weight |a| go to slot
+ *                 cache_lens[b] (the caller advances cache_lens).  Zero: the token is only scored.
+ *  av             [B, H*hd] fp32 output; rows of inactive sequences are zero
+ *  workspace      hstu_paged_attention_workspace_size(shape) bytes, 256-byte aligned
+ * With cache->weights, |a_j| is added to each cached token's weight, also when append is zero.  The
+ * result does not depend on the order of anything that runs: repeated calls agree bit for bit.
+ */
+size_t hstu_paged_attention_workspace_size(const hstu_shape_t* shape);
+hstu_status_t hstu_paged_attention_fwd(const hstu_shape_t* shape, const hstu_paged_cache_t* cache,
+                                       const void* uvqk, const int32_t* page_table,
+                                       int64_t max_pages, const int64_t* cache_lens,
+                                       const int64_t* next_positions, const int64_t* timestamps,
+                                       const float* pos_table, const float* time_table,
+                                       const float* alibi_slopes, float scale, int32_t append,
+                                       void* av, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/*
+ * hstu_paged_layer_fwd -- one HSTU layer (Eqs. 1-3) over one new token a sequence: f1 of X [B, d], the
+ * attention above, LayerNorm * U, f2 and the residual, into out [B, d].  Other arguments as for
+ * hstu_paged_attention_fwd and hstu_layer_fwd; workspace: hstu_paged_layer_workspace_size(shape)
+ * bytes.  Inactive rows give the row of an AV of zero.
+ */
+size_t hstu_paged_layer_workspace_size(const hstu_shape_t* shape);
+hstu_status_t hstu_paged_layer_fwd(const hstu_shape_t* shape, const hstu_paged_cache_t* cache,
+                                   const void* X, const int32_t* page_table, int64_t max_pages,
+                                   const int64_t* cache_lens, const int64_t* next_positions,
+                                   const int64_t* timestamps, const void* W1, const void* b1,
+                                   const void* W2, const void* b2, const void* ln_w,
+                                   const void* ln_b, const float* pos_table,
+                                   const float* time_table, const float* alibi_slopes, float scale,
+                                   int32_t append, void* out, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * hstu_cache_evict -- cuts every sequence with more than `budget` cached tokens to `budget`: first the
+ * tokens at positions >= next_positions[b] - recent are kept, then those with the largest weight
+ * fp32(sum over the heads), then, of equal ones, those in the lower slots (NaN weights last).
+ * The kept tokens in slots >= budget move, in ascending order, into the slots below it that became
+ * free, with K, V, position, timestamp and weights; nothing else of the cache is written, and the
+ * pages from ceil(budget / page_size) on are the caller's again.
+ *
+ *  page_table     [num_seqs, max_pages] int32        cache_lens [num_seqs] int64
+ *  next_positions [num_seqs] int64, or NULL: cache_lens
+ *  budget         >= 0        recent   0 .. budget
+ *  new_lens       [num_seqs] int64 output: min(cache_lens[b], budget), inactive rows unchanged; may
+ *                 be cache_lens itself
+ *  workspace      hstu_cache_evict_workspace_size(cache, num_seqs, max_pages) bytes, 256-byte aligned
+ * The cache needs positions and weights.  The result does not depend on the order of anything that
+ * runs.  Asynchronous on `stream`.
+ */
+size_t hstu_cache_evict_workspace_size(const hstu_paged_cache_t* cache, int64_t num_seqs,
+                                       int64_t max_pages);
+hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs,
+                               const int32_t* page_table, int64_t max_pages,
+                               const int64_t* cache_lens, const int64_t* next_positions,
+                               int64_t budget, int64_t recent, int64_t* new_lens, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /*
  * Stochastic Length ("Actions Speak Louder than Words" paper notes, section 3.3): shortens the
