@@ -381,10 +381,12 @@ paged::Cache cache_view(const hstu_paged_cache_t& c) {
   return {c.k, c.v, c.positions, c.timestamps, c.weights, c.num_pages, shift, c.num_heads};
 }
 
-hstu_status_t check_table(int64_t num_seqs, const int32_t* page_table, int64_t max_pages,
-                          const int64_t* cache_lens) {
+hstu_status_t check_table(int page_size, int64_t num_seqs, const int32_t* page_table,
+                          int64_t max_pages, const int64_t* cache_lens) {
   if (num_seqs < 0 || max_pages < 0 || max_pages >= (1LL << 31)) return HSTU_ERR_INVALID_ARG;
   if (num_seqs > 0 && (!page_table || !cache_lens || max_pages == 0)) return HSTU_ERR_INVALID_ARG;
+  // slots of a sequence are numbered in 32 bits
+  if (max_pages * page_size >= (1LL << 31)) return HSTU_ERR_UNSUPPORTED;
   return HSTU_OK;
 }
 
@@ -403,7 +405,7 @@ hstu_status_t check_paged(const hstu_shape_t* shape, const hstu_paged_cache_t* c
       cache->dtype != s.dtype || s.max_seq_len < 1)
     return HSTU_ERR_INVALID_ARG;
   if (s.num_seqs * (int64_t)s.num_heads >= (1LL << 31)) return HSTU_ERR_UNSUPPORTED;
-  if ((rc = check_table(s.num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
+  if ((rc = check_table(cache->page_size, s.num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
   if ((rc = check_bias(shape, timestamps, pos, tim, alibi, scale)) != HSTU_OK) return rc;
   if (tim && !cache->timestamps) return HSTU_ERR_INVALID_ARG;
   if (append && cache->timestamps && !timestamps) return HSTU_ERR_INVALID_ARG;
@@ -434,8 +436,7 @@ hstu_status_t run_paged_attention(const hstu_shape_t& s, const hstu_paged_cache_
   a.B = s.num_seqs;
   a.max_len = s.max_seq_len - 1;
   a.av = (float*)av;
-  (void)ws;
-  return paged::launch_attention(a, s.dtype, s.d_qk, st);
+  return paged::launch_attention(a, s.dtype, s.d_qk, ws, tc::num_sms(), st);
 }
 
 struct PagedWorkspace {
@@ -1067,7 +1068,7 @@ hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seq
   hstu_status_t rc = check_cache(cache);
   if (rc != HSTU_OK) return rc;
   if (total_tokens < 0 || total_tokens > (1LL << 40)) return HSTU_ERR_INVALID_ARG;
-  if ((rc = check_table(num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
+  if ((rc = check_table(cache->page_size, num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
   if (total_tokens == 0) return HSTU_OK;
   if (num_seqs == 0 || !uvqk || !seq_offsets || !aligned16(uvqk)) return HSTU_ERR_INVALID_ARG;
   if (cache->timestamps && !timestamps) return HSTU_ERR_INVALID_ARG;
@@ -1085,7 +1086,7 @@ hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seq
 
 size_t hstu_paged_attention_workspace_size(const hstu_shape_t* shape) {
   if (check_shape(shape) != HSTU_OK) return 0;
-  return 0;
+  return align_up(paged::attention_workspace_bytes(shape->d_v));
 }
 
 hstu_status_t hstu_paged_attention_fwd(const hstu_shape_t* shape, const hstu_paged_cache_t* cache,
@@ -1171,7 +1172,7 @@ hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs
   if (rc != HSTU_OK) return rc;
   if (budget < 0 || recent < 0 || recent > budget) return HSTU_ERR_INVALID_ARG;
   if (!cache->positions || !cache->weights) return HSTU_ERR_INVALID_ARG;
-  if ((rc = check_table(num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
+  if ((rc = check_table(cache->page_size, num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
   if (num_seqs == 0) return HSTU_OK;
   if (num_seqs > 65535) return HSTU_ERR_UNSUPPORTED;
   if (!new_lens || !workspace) return HSTU_ERR_INVALID_ARG;
