@@ -10,6 +10,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace hstu {
 namespace paged {
@@ -74,28 +75,22 @@ __device__ __forceinline__ int time_bucket(int64_t dt, int Tb) {
   return b < Tb ? b : Tb - 1;
 }
 
-// 16 bytes of T as fp32.
+// 16 bytes of T as pairs of fp32.
 template <typename T> struct vec16;
 template <> struct vec16<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void widen(const uint4& u, float* f) {
-    f[0] = __uint_as_float(u.x);
-    f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z);
-    f[3] = __uint_as_float(u.w);
+  static __device__ __forceinline__ void widen(const uint4& u, uint64_t (&f)[2]) {
+    f[0] = sm100::f2_pack(__uint_as_float(u.x), __uint_as_float(u.y));
+    f[1] = sm100::f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
   }
 };
 template <> struct vec16<bf16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void widen(const uint4& u, float* f) {
-    f[0] = bf16_lo(u.x);
-    f[1] = bf16_hi(u.x);
-    f[2] = bf16_lo(u.y);
-    f[3] = bf16_hi(u.y);
-    f[4] = bf16_lo(u.z);
-    f[5] = bf16_hi(u.z);
-    f[6] = bf16_lo(u.w);
-    f[7] = bf16_hi(u.w);
+  static __device__ __forceinline__ void widen(const uint4& u, uint64_t (&f)[4]) {
+    f[0] = sm100::f2_pack(bf16_lo(u.x), bf16_hi(u.x));
+    f[1] = sm100::f2_pack(bf16_lo(u.y), bf16_hi(u.y));
+    f[2] = sm100::f2_pack(bf16_lo(u.z), bf16_hi(u.z));
+    f[3] = sm100::f2_pack(bf16_lo(u.w), bf16_hi(u.w));
   }
 };
 
@@ -107,12 +102,22 @@ template <> struct vec16<bf16> {
 // The unit of work is a tile of TILE rows of one (sequence, head): 4 KB of K and 4 KB of V.  All
 // tiles of the batch, in the order (sequence, head, tile), are dealt to the warps of a persistent
 // grid in equal contiguous ranges, so that one long history and many ragged ones load the SMs
-// alike; every CTA finds its ranges from the lengths itself (one block scan).  A warp that holds
-// all tiles of a (sequence, head) writes its row of AV; parts are joined first among the CTA's
-// warps in shared memory, then, where a (sequence, head) spans CTAs, by a second kernel, always in
-// the same order.
-constexpr int ATTN_THREADS = 512;
-constexpr int ATTN_WARPS = ATTN_THREADS / 32;
+// alike; every CTA finds its ranges from the lengths itself (one block scan).  Each warp brings its
+// tiles into its own ring in shared memory by bulk copies.  A warp that holds all tiles of a
+// (sequence, head) writes its row of AV; parts are joined first among the CTA's warps in shared
+// memory, then, where a (sequence, head) spans CTAs, by a second kernel, always in the same order.
+constexpr int ATTN_WARPS = 12;
+constexpr int ATTN_STAGES = 2;
+constexpr int ATTN_THREADS = ATTN_WARPS * 32;
+constexpr int ATTN_HALF = 4096;                 // bytes of a tile's K, and of its V
+template <int HD> struct AttnSmem {
+  static constexpr int RING = ATTN_WARPS * ATTN_STAGES * 2 * ATTN_HALF;
+  static constexpr int PARTS = ATTN_WARPS * 2 * HD * 4;
+  static constexpr int TOTAL = RING + PARTS + 128;   // + alignment
+};
+
+// CTAs of the attention: one a SM, at most this many (the workspace holds a part record for each).
+constexpr int ATTN_MAX_CTAS = 256;
 
 // What a CTA leaves for the joining kernel.
 struct Part {
@@ -128,18 +133,44 @@ struct Tile {
   int pg[NP];
 };
 
+// Copies `bytes` (a multiple of 16, both addresses 16-byte aligned) and counts them on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          sm100::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+
+// a / b for 0 <= a, 0 < b; the 64-bit division takes several times as long as the 32-bit one.
+__device__ __forceinline__ int64_t div_by(int64_t a, int b) {
+  return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a, float* parts, Part* recs) {
+  using sm100::f2_add;
+  using sm100::f2_fma;
+  using sm100::f2_pack;
+  using sm100::f2_unpack;
   constexpr int E = vec16<T>::N;      // elements a lane holds of a row
   constexpr int LPR = HD / E;         // lanes a row
   constexpr int RPI = 32 / LPR;       // rows a warp-wide load
   constexpr int TILE = 8 * RPI;
   constexpr int NP = TILE > 16 ? TILE / 16 : 1;
+  constexpr int PIECE = TILE / NP;    // rows a piece
+  constexpr int ROW = HD * (int)sizeof(T);
   static_assert(LPR >= 8 && LPR <= 32, "a row spans 8 to 32 lanes");
+  static_assert(TILE * ROW == ATTN_HALF, "a tile is 4 KB of K");
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((128 - (sm100::smem_u32(smem_raw) & 127)) & 127);
+  float(*sp)[2][HD] = reinterpret_cast<float(*)[2][HD]>(smem + AttnSmem<HD>::RING);
   __shared__ int64_t pre[ATTN_THREADS];
+  __shared__ int s_len[ATTN_THREADS];
   __shared__ int64_t scratch[ATTN_WARPS];
-  __shared__ __align__(16) float sp[ATTN_WARPS][2][HD];
   __shared__ int s_before[ATTN_WARPS], s_pair[ATTN_WARPS];
+  __shared__ __align__(8) uint64_t bars[ATTN_WARPS][ATTN_STAGES];
+  __shared__ int s_abort;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int sub = lane % LPR, grp = lane / LPR;
   const int H = a.c.H, shift = a.c.ps_shift, ps = 1 << shift, B = (int)a.B;
@@ -147,11 +178,26 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
   const int64_t most = a.max_len < room ? a.max_len : room;
   auto tiles_of = [&](int n) { return n < 0 ? 0 : n / TILE + 1; };   // of n cached rows and the new one
 
-  // tiles a head before each group of C sequences
+  if (lane == 0) {
+    s_before[warp] = 0;
+    s_pair[warp] = -1;
+#pragma unroll
+    for (int k = 0; k < ATTN_STAGES; k++) sm100::mbar_init(&bars[warp][k], 1);
+    sm100::fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    recs[blockIdx.x] = {-1, 0};
+  }
+  // tiles a head up to each group of C sequences; with C = 1 the lengths stay in shared memory
   const int C = (B + ATTN_THREADS - 1) / ATTN_THREADS;
   int64_t sum = 0;
-  for (int b = threadIdx.x * C; b < B && b < (threadIdx.x + 1) * C; b++)
-    sum += tiles_of((int)cached_len(a.lens[b], most));
+  int n_one = -1;
+  for (int b = threadIdx.x * C; b < B && b < (threadIdx.x + 1) * C; b++) {
+    n_one = (int)cached_len(a.lens[b], most);
+    sum += tiles_of(n_one);
+  }
+  s_len[threadIdx.x] = n_one;
   {
     int64_t x = sum;
 #pragma unroll
@@ -161,77 +207,70 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
     }
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
-    if (warp == 0 && lane < ATTN_WARPS) {
-      int64_t w = scratch[lane];
+    int64_t before = 0;
 #pragma unroll
-      for (int o = 1; o < ATTN_WARPS; o <<= 1) {
-        const int64_t y = __shfl_up_sync((1u << ATTN_WARPS) - 1u, w, o);
-        if (lane >= o) w += y;
-      }
-      scratch[lane] = w;
-    }
-    __syncthreads();
-    pre[threadIdx.x] = x + (warp ? scratch[warp - 1] : 0);
+    for (int w = 0; w < ATTN_WARPS; w++) before += w < warp ? scratch[w] : 0;
+    pre[threadIdx.x] = x + before;
     __syncthreads();
   }
+  auto length = [&](int b) { return C == 1 ? s_len[b] : (int)cached_len(a.lens[b], most); };
+  // every warp's share: `share` tiles, one more for the first `over` warps
   const int64_t units = pre[ATTN_THREADS - 1] * H;
-  const int64_t gw = (int64_t)blockIdx.x * ATTN_WARPS + warp, W = (int64_t)gridDim.x * ATTN_WARPS;
-  const int64_t u0 = units * gw / W, u1 = units * (gw + 1) / W;
+  const int gw = blockIdx.x * ATTN_WARPS + warp, W = gridDim.x * ATTN_WARPS;
+  const int64_t share = div_by(units, W);
+  const int over = (int)(units - share * W);
+  const int64_t u0 = gw * share + (gw < over ? gw : over), u1 = u0 + share + (gw < over ? 1 : 0);
 
-  if (lane == 0) {
-    s_before[warp] = 0;
-    s_pair[warp] = -1;
-  }
-  if (threadIdx.x == 0) recs[blockIdx.x] = {-1, 0};
   if (u0 < u1) {
     using Tl = Tile<NP>;
-    auto length = [&](int b) { return (int)cached_len(a.lens[b], most); };
     auto pages = [&](Tl& t) {
       const int32_t* row = a.table + (int64_t)t.b * a.max_pages;
 #pragma unroll
       for (int p = 0; p < NP; p++) {
-        const int j = t.i * TILE + 16 * p;
+        const int j = t.i * TILE + PIECE * p;
         t.pg[p] = j < t.n ? (int)page_of(row, j >> shift, a.c.num_pages) : -1;
       }
     };
-    // the first unit: its group by bisection, its sequence by scans over 32 lengths at a time
+    // the first unit: its group by comparing every ATTN_WARPS-th sum, then the sums between, and
+    // with more than one sequence a group by scans over 32 lengths at a time
     Tl cur;
     {
-      const int64_t v = u0 / H;
-      int lo = 0, hi = ATTN_THREADS - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (pre[mid] > v) hi = mid; else lo = mid + 1;
-      }
+      const int64_t v = div_by(u0, H);
+      const unsigned c1 = __ballot_sync(0xffffffffu, pre[lane * ATTN_WARPS + ATTN_WARPS - 1] > v);
+      const int g = c1 ? __ffs(c1) - 1 : 31;
+      const unsigned c2 = __ballot_sync(0xffffffffu, lane < ATTN_WARPS && pre[g * ATTN_WARPS + lane % ATTN_WARPS] > v);
+      const int lo = g * ATTN_WARPS + (c2 ? __ffs(c2) - 1 : ATTN_WARPS - 1);
       int64_t base = lo ? pre[lo - 1] : 0;
-      int b0 = lo * C;
-      cur.b = B - 1;
-      while (b0 < B) {   // ends with a hit: v is below the batch's tiles
-        const int b = b0 + lane;
-        const int t = b < B ? tiles_of(length(b)) : 0;
-        int64_t x = t;
+      cur.b = lo < B ? lo : B - 1;
+      if (C > 1) {
+        int b0 = lo * C;
+        cur.b = B - 1;
+        while (b0 < B) {   // ends with a hit: v is below the batch's tiles
+          const int b = b0 + lane;
+          const int t = b < B ? tiles_of(length(b)) : 0;
+          int64_t x = t;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, base + x > v);
+          if (hit) {
+            const int f = __ffs(hit) - 1;
+            cur.b = b0 + f;
+            base += __shfl_sync(0xffffffffu, x - t, f);
+            break;
+          }
+          base += __shfl_sync(0xffffffffu, x, 31);
+          b0 += 32;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, base + x > v);
-        if (hit) {
-          const int f = __ffs(hit) - 1;
-          cur.b = b0 + f;
-          base += __shfl_sync(0xffffffffu, x - t, f);
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, x, 31);
-        b0 += 32;
       }
       cur.n = length(cur.b);
       cur.tiles = cur.n < 0 ? 1 : tiles_of(cur.n);
       const int64_t r = u0 - base * H;
-      cur.h = (int)(r / cur.tiles);
-      cur.i = (int)(r % cur.tiles);
+      cur.h = (int)div_by(r, cur.tiles);
+      cur.i = (int)(r - (int64_t)cur.h * cur.tiles);
     }
-    pages(cur);
     auto advance = [&](Tl& t) {
       if (++t.i == t.tiles) {
         t.i = 0;
@@ -242,87 +281,127 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
           t.tiles = tiles_of(t.n);
         }
       }
-      pages(t);
     };
     auto u_row = [&](const Tl& t, int block) {   // the new token's U, V, Q or K of the head
-      return static_cast<const T*>(a.uvqk) + ((int64_t)t.b * 4 + block) * H * HD + (int64_t)t.h * HD + sub * E;
+      return static_cast<const T*>(a.uvqk) + (((int64_t)t.b * 4 + block) * H + t.h) * HD;
     };
-    // rows of K (block 3) or V (block 1) of a tile
-    auto load = [&](const Tl& t, const void* pool, int block, uint4 (&r)[8]) {
-      const T* base[NP];
-      bool full = (t.i + 1) * TILE <= t.n;
+    unsigned char* ring = smem + warp * (ATTN_STAGES * 2 * ATTN_HALF);
+    // the tile's K and V rows, piece by piece, and the new token's into the row after the last
+    auto issue = [&](const Tl& t, int stage) {
+      if (lane == 0) {
+        uint64_t* bar = &bars[warp][stage];
+        unsigned char* dst = ring + stage * 2 * ATTN_HALF;
+        int rows[NP], total = 0;
 #pragma unroll
-      for (int p = 0; p < NP; p++) {
-        const int o = (t.i * TILE + 16 * p) & (ps - 1);
-        base[p] = static_cast<const T*>(pool) + ((((int64_t)t.pg[p] * H + t.h) << shift) + o - 16 * p + grp) * HD + sub * E;
-        full = full && t.pg[p] >= 0;
-      }
-      if (full) {
+        for (int p = 0; p < NP; p++) {
+          const int left = t.n - (t.i * TILE + PIECE * p);
+          rows[p] = t.pg[p] < 0 || left <= 0 ? 0 : (left < PIECE ? left : PIECE);
+          total += rows[p];
+        }
+        const bool own = t.i == t.tiles - 1;
+        sm100::mbar_arrive_expect_tx(bar, (uint32_t)(total + own) * 2 * ROW);
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-          r[i] = *reinterpret_cast<const uint4*>(base[i * RPI / 16] + i * RPI * HD);
-      } else {
-        const T* own = u_row(t, block);
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const int j = t.i * TILE + i * RPI + grp;
-          r[i] = make_uint4(0, 0, 0, 0);
-          if (j < t.n) {
-            if (t.pg[i * RPI / 16] >= 0)
-              r[i] = *reinterpret_cast<const uint4*>(base[i * RPI / 16] + i * RPI * HD);
-          } else if (j == t.n) {
-            r[i] = *reinterpret_cast<const uint4*>(own);
-          }
+        for (int p = 0; p < NP; p++) {
+          if (rows[p] == 0) continue;
+          const int64_t at = ((((int64_t)t.pg[p] * H + t.h) << shift) + ((t.i * TILE + PIECE * p) & (ps - 1))) * HD;
+          bulk_load(dst + p * PIECE * ROW, static_cast<const T*>(a.c.k) + at, rows[p] * ROW, bar);
+          bulk_load(dst + ATTN_HALF + p * PIECE * ROW, static_cast<const T*>(a.c.v) + at, rows[p] * ROW, bar);
+        }
+        if (own) {
+          const int o = (t.n - t.i * TILE) * ROW;
+          bulk_load(dst + o, u_row(t, 3), ROW, bar);
+          bulk_load(dst + ATTN_HALF + o, u_row(t, 1), ROW, bar);
         }
       }
     };
-    // the lane's own row of a tile after the exchange of partial sums
+    // What the lane needs for the row of a tile that is its own after the exchange of partial sums
+    // comes in two steps: position, time and weight two tiles ahead (they need the page), the
+    // biases they select one tile ahead.
     const int mine = (sub % 8) * RPI + grp;
-    struct Meta {
-      int32_t p;
-      int64_t t;
+    struct Raw {
+      int p;
       float w;
+      int64_t t;
+    };
+    struct Own {
+      float bias, w;
     };
     auto own_page = [&](const Tl& t) { return NP > 1 && mine >= 16 ? t.pg[NP - 1] : t.pg[0]; };
-    auto load_meta = [&](const Tl& t, Meta& m) {
+    int p_new = 0;         // position and time of the new token of the tile last looked up
+    int64_t t_new = 0;
+    auto load_raw = [&](const Tl& t, bool fresh) {
+      if (fresh) {
+        const int64_t p = a.next_pos ? a.next_pos[t.b] : t.n;
+        if (p < 0 || p > 0x7fffffff) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
+        p_new = p < 0 ? 0 : (p > 0x7fffffff ? 0x7fffffff : (int)p);
+        t_new = a.now ? a.now[t.b] : 0;
+      }
       const int j = t.i * TILE + mine, pg = own_page(t);
-      m.p = j;
-      m.t = 0;
-      m.w = 0.0f;
+      Raw m{j, 0.0f, 0};
       if (j < t.n && pg >= 0) {
         const int64_t s = ((int64_t)pg << shift) + (j & (ps - 1));
         if (a.c.positions && (a.pos || a.alibi)) m.p = a.c.positions[s];
         if (a.tim) m.t = a.c.timestamps[s];
         if (a.c.weights) m.w = a.c.weights[(((int64_t)pg * H + t.h) << shift) + (j & (ps - 1))];
+      } else {
+        m.p = p_new;
+        m.t = t_new;
       }
+      return m;
     };
-    uint4 k[8], v[8], q = *reinterpret_cast<const uint4*>(u_row(cur, 2));
-    float acc[E];
-#pragma unroll
-    for (int e = 0; e < E; e++) acc[e] = 0.0f;
-    Meta meta;
-    load(cur, a.c.k, 3, k);
-    load_meta(cur, meta);
-    Tl nxt = cur;
+    auto look_up = [&](const Tl& t, const Raw& m) {
+      Own r{0.0f, m.w};
+      const int far = p_new - m.p, dist = far < 0 ? 0 : far;
+      if (a.pos) r.bias = a.pos[(int64_t)t.h * a.P + (dist < a.P ? dist : a.P - 1)];
+      if (a.tim) r.bias += a.tim[(int64_t)t.h * a.Tb + time_bucket(t_new - m.t, a.Tb)];
+      if (a.alibi) r.bias = -a.alibi[t.h] * (float)dist;
+      return r;
+    };
+    auto load_query = [&](const Tl& t) {
+      return *reinterpret_cast<const uint4*>(u_row(t, 2) + sub * E);
+    };
+    // nxt: the tile after cur, in flight; far: the one after that, its pages being looked up
+    Tl nxt = cur, far;
     if (u0 + 1 < u1) advance(nxt);
+    far = nxt;
+    if (u0 + 2 < u1) advance(far);
+    pages(cur);
+    pages(nxt);
+    pages(far);
+    uint4 query = load_query(cur);
+    __syncwarp();
+    issue(cur, 0);
+    if (u0 + 1 < u1) issue(nxt, 1);
+    Raw raw = load_raw(cur, true);
+    Own own = look_up(cur, raw);
+    if (u0 + 1 < u1) raw = load_raw(nxt, nxt.i == 0);
+    uint64_t acc[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; e++) acc[e] = 0;
     bool whole = cur.i == 0;   // acc holds the (sequence, head) from its first tile on
+    int stage = 0, parity = 0;
+    bool ok = true;
     for (int64_t u = u0; u < u1; u++) {
-      load(cur, a.c.v, 1, v);
-      float part[8], f[E], qf[E];
-      vec16<T>::widen(q, qf);
+      const bool more = u + 1 < u1;
+      const uint4 y = query;
+      if (more && nxt.i == 0) query = load_query(nxt);
+      const bool full = (cur.i + 1) * TILE <= cur.n && cur.pg[0] >= 0 && cur.pg[NP - 1] >= 0;
+      const uint4* ks = reinterpret_cast<const uint4*>(ring + stage * 2 * ATTN_HALF) + lane;
+      const uint4* vs = ks + ATTN_HALF / 16;
+      ok = sm100::mbar_wait(&bars[warp][stage], parity, &s_abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      uint64_t f[E / 2], qf[E / 2];
+      float part[8];
+      vec16<T>::widen(y, qf);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        vec16<T>::widen(k[i], f);
-        part[i] = 0.0f;
+        vec16<T>::widen(ks[i * 32], f);
+        uint64_t d = sm100::f2_mul(qf[0], f[0]);
 #pragma unroll
-        for (int e = 0; e < E; e++) part[i] = fmaf(qf[e], f[e], part[i]);
-      }
-      const Meta m = meta;
-      const bool more = u + 1 < u1;
-      if (more) {
-        load(nxt, a.c.k, 3, k);
-        load_meta(nxt, meta);
-        if (nxt.i == 0) q = *reinterpret_cast<const uint4*>(u_row(nxt, 2));
+        for (int e = 1; e < E / 2; e++) d = f2_fma(qf[e], f[e], d);
+        float lo, hi;
+        f2_unpack(d, lo, hi);
+        part[i] = lo + hi;
       }
       // 8 rows a lane over 8 lanes: each exchange halves the rows a lane sums, so that lane `sub`
       // ends up with row sub % 8 of its group; wider rows add the remaining lanes' sums
@@ -338,115 +417,134 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
 #pragma unroll
       for (int w = 8; w < LPR; w <<= 1) part[0] += __shfl_xor_sync(0xffffffffu, part[0], w);
       const int j = cur.i * TILE + mine, pg = own_page(cur);
-      const int64_t p_new = a.next_pos ? a.next_pos[cur.b] : cur.n;
       float wgt = 0.0f;
       if (j == cur.n || (j < cur.n && pg >= 0)) {
-        int64_t dist = 0, dt = 0;
-        if (j < cur.n) {
-          dist = p_new - m.p;
-          if (dist < 0) dist = 0;
-          if (a.tim) dt = a.now[cur.b] - m.t;
-        }
-        float x = part[0];
-        if (a.pos) x += a.pos[(int64_t)cur.h * a.P + (dist < a.P ? dist : a.P - 1)];
-        if (a.tim) x += a.tim[(int64_t)cur.h * a.Tb + time_bucket(dt, a.Tb)];
-        if (a.alibi) x -= a.alibi[cur.h] * (float)dist;
+        const float x = part[0] + own.bias;
         wgt = a.scale * silu_accurate(x);
         if (a.c.weights && j < cur.n && sub < 8)
-          a.c.weights[(((int64_t)pg * H + cur.h) << shift) + (j & (ps - 1))] = m.w + fabsf(wgt);
+          a.c.weights[(((int64_t)pg * H + cur.h) << shift) + (j & (ps - 1))] = own.w + fabsf(wgt);
       }
+      if (more) own = look_up(nxt, raw);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const float w = __shfl_sync(0xffffffffu, wgt, grp * LPR + i);
-        vec16<T>::widen(v[i], f);
+        uint4 r = vs[i * 32];
+        if (!full) {
+          // rows past the new token's, or of no page, hold what was there before
+          const int jr = cur.i * TILE + i * RPI + grp;
+          if (jr > cur.n || (jr < cur.n && cur.pg[i * RPI / 16] < 0)) r = make_uint4(0, 0, 0, 0);
+        }
+        vec16<T>::widen(r, f);
+        const uint64_t ww = f2_pack(w, w);
 #pragma unroll
-        for (int e = 0; e < E; e++) acc[e] = fmaf(w, f[e], acc[e]);
+        for (int e = 0; e < E / 2; e++) acc[e] = f2_fma(ww, f[e], acc[e]);
       }
       const bool last = cur.i == cur.tiles - 1;
       if (last && a.append && a.lens[cur.b] == cur.n && cur.n <= room) {
-        // the new row joins the cache: the lane that owns it writes its weight (and, for head 0,
-        // position and time), lanes of one row piece each copy K and V
+        // the new row joins the cache: one row piece's lanes copy K and V, the lane that owns the
+        // row writes its weight and, for head 0, position and time
         const int64_t to = page_of(a.table + (int64_t)cur.b * a.max_pages, cur.n >> shift, a.c.num_pages);
         const int64_t o = cur.n & (ps - 1);
         if (to >= 0) {
           const int64_t r = ((to * H + cur.h) << shift) + o;
           if (grp == 0) {
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.c.k) + r * HD + sub * E) =
-                *reinterpret_cast<const uint4*>(u_row(cur, 3));
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.c.v) + r * HD + sub * E) =
-                *reinterpret_cast<const uint4*>(u_row(cur, 1));
+            const int at = (cur.n - cur.i * TILE) * LPR + sub - lane;
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.c.k) + r * HD + sub * E) = ks[at];
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.c.v) + r * HD + sub * E) = vs[at];
           }
           if (j == cur.n && sub < 8) {
             if (a.c.weights) a.c.weights[r] = fabsf(wgt);
             if (cur.h == 0) {
-              if (a.c.positions) a.c.positions[(to << shift) + o] = (int32_t)p_new;
+              if (a.c.positions)
+                a.c.positions[(to << shift) + o] = (int32_t)(a.next_pos ? a.next_pos[cur.b] : cur.n);
               if (a.c.timestamps && a.now) a.c.timestamps[(to << shift) + o] = a.now[cur.b];
             }
           }
         }
       }
+      __syncwarp();   // every lane has read the stage
+      if (u + 2 < u1) {
+        issue(far, stage);
+        raw = load_raw(far, far.i == 0);
+      }
       if (last || !more) {
+        float s[E];
+#pragma unroll
+        for (int e = 0; e < E / 2; e++) f2_unpack(acc[e], s[2 * e], s[2 * e + 1]);
 #pragma unroll
         for (int w = LPR; w < 32; w <<= 1)
 #pragma unroll
-          for (int e = 0; e < E; e++) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], w);
+          for (int e = 0; e < E; e++) s[e] += __shfl_xor_sync(0xffffffffu, s[e], w);
         const int pair = cur.b * H + cur.h;
         float* to = last && whole ? a.av + (int64_t)pair * HD : sp[warp][whole];
         if (grp == 0) {
 #pragma unroll
           for (int e = 0; e < E; e += 4)
-            *reinterpret_cast<float4*>(to + sub * E + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+            *reinterpret_cast<float4*>(to + sub * E + e) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
         }
         if (lane == 0) {
           if (!whole) s_before[warp] = last ? 2 : 1;
           else if (!last) s_pair[warp] = pair;
         }
 #pragma unroll
-        for (int e = 0; e < E; e++) acc[e] = 0.0f;
+        for (int e = 0; e < E / 2; e++) acc[e] = 0;
         whole = true;
       }
-      if (more) {
-        cur = nxt;
-        if (u + 2 < u1) advance(nxt);
+      cur = nxt;
+      nxt = far;
+      if (u + 3 < u1) {
+        advance(far);
+        pages(far);
       }
+      stage ^= 1;
+      parity ^= stage == 0;
+    }
+    if (!__all_sync(0xffffffffu, ok)) {
+      // gave up: what is still being copied lands before the CTA goes
+      sm100::mbar_drain(&bars[warp][stage], parity);
+      sm100::mbar_drain(&bars[warp][stage ^ 1], parity ^ (stage == 1));
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // rows of inactive sequences
   for (int b = blockIdx.x; b < B; b += gridDim.x)
-    if (a.lens[b] < 0)
+    if (length(b) < 0)
       for (int i = threadIdx.x; i < H * HD; i += ATTN_THREADS) a.av[(int64_t)b * H * HD + i] = 0.0f;
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // a warp's open end is followed by the later warps' parts, up to the one that ends it
-  for (int start = warp == 0 ? -1 : warp; start <= warp; start++) {
-    // start -1: the part that began in an earlier CTA
-    if (start >= 0 && s_pair[start] < 0) continue;
-    bool any = start >= 0, ends = false;
-    float s[(HD + 31) / 32];
+  // A warp's open end is followed by the later warps' parts, up to the one that ends it.  Parts that
+  // began in an earlier CTA come before the first open end.
+  const int flag = lane < ATTN_WARPS ? s_before[lane] : 0;
+  const unsigned parted = __ballot_sync(0xffffffffu, flag != 0), ends = __ballot_sync(0xffffffffu, flag == 2);
+  auto add_parts = [&](unsigned set, bool open, float* to) {
+    float s[HD / 32];
 #pragma unroll
-    for (int e = 0; e < HD / 32; e++) s[e] = start >= 0 ? sp[start][1][lane + 32 * e] : 0.0f;
-    for (int w = start + 1; w < ATTN_WARPS && !ends; w++) {
-      // a part from before this warp belongs to the chain; a warp that begins anew has none
-      if (s_before[w]) {
-        any = true;
+    for (int e = 0; e < HD / 32; e++) s[e] = open ? sp[warp][1][lane + 32 * e] : 0.0f;
+    for (; set; set &= set - 1) {
+      const int w = __ffs(set) - 1;
 #pragma unroll
-        for (int e = 0; e < HD / 32; e++) s[e] += sp[w][0][lane + 32 * e];
-        ends = s_before[w] == 2;
-      }
-      if (start < 0 && s_pair[w] >= 0) break;
+      for (int e = 0; e < HD / 32; e++) s[e] += sp[w][0][lane + 32 * e];
     }
-    if (start < 0) {
-      if (lane == 0) recs[blockIdx.x].before = any ? (ends ? 2 : 1) : 0;
-      if (any)
 #pragma unroll
-        for (int e = 0; e < HD / 32; e++) parts[(int64_t)blockIdx.x * 2 * HD + lane + 32 * e] = s[e];
-    } else if (ends) {
-#pragma unroll
-      for (int e = 0; e < HD / 32; e++) a.av[(int64_t)s_pair[start] * HD + lane + 32 * e] = s[e];
-    } else {
-      if (lane == 0) recs[blockIdx.x].pair = s_pair[start];
-#pragma unroll
-      for (int e = 0; e < HD / 32; e++) parts[((int64_t)blockIdx.x * 2 + 1) * HD + lane + 32 * e] = s[e];
+    for (int e = 0; e < HD / 32; e++) to[lane + 32 * e] = s[e];
+  };
+  auto up_to_end = [&](unsigned set) {   // the set's warps up to its first end
+    const unsigned e = set & ends;
+    return e ? set & ((e & (0u - e)) * 2u - 1u) : set;
+  };
+  const int pair = s_pair[warp];
+  if (pair >= 0) {
+    const unsigned set = up_to_end(parted & ~((2u << warp) - 1u));
+    const bool done = set & ends;
+    add_parts(set, true, done ? a.av + (int64_t)pair * HD : parts + ((int64_t)blockIdx.x * 2 + 1) * HD);
+    if (!done && lane == 0) recs[blockIdx.x].pair = pair;
+  }
+  if (warp == 0) {
+    const unsigned opens = __ballot_sync(0xffffffffu, lane < ATTN_WARPS && s_pair[lane] >= 0);
+    const unsigned first = opens & (0u - opens);   // its own part from before may end there too
+    const unsigned set = up_to_end(opens ? parted & (first * 2u - 1u) : parted);
+    if (set) {
+      add_parts(set, false, parts + (int64_t)blockIdx.x * 2 * HD);
+      if (lane == 0) recs[blockIdx.x].before = set & ends ? 2 : 1;
     }
   }
 }
@@ -454,23 +552,24 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
 // Joins the parts of the (sequence, head)s that span CTAs, one CTA for each CTA of the attention: its
 // open part and the parts of the following CTAs up to the one that ends it, summed in a fixed order.
 template <int HD>
-__global__ void __launch_bounds__(256) attention_join_kernel(float* av, const float* parts,
+__global__ void __launch_bounds__(ATTN_MAX_CTAS) attention_join_kernel(float* av, const float* parts,
                                                              const Part* recs, int ctas) {
-  constexpr int L = HD / 4, G = 256 / L;   // lanes a row, rows at a time
-  __shared__ int s_end;
+  constexpr int L = HD / 4, G = ATTN_MAX_CTAS / L;   // lanes a row, rows at a time
+  __shared__ int s_end, s_flag[ATTN_MAX_CTAS];
   __shared__ float4 red[G][L];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, pair = recs[c].pair;
-  if (pair < 0) return;
   if (threadIdx.x == 0) s_end = ctas - 1;
+  const int flag = threadIdx.x < ctas ? recs[threadIdx.x].before : 0;
+  s_flag[threadIdx.x] = flag;
+  if (pair < 0) return;
   __syncthreads();
-  for (int k = c + 1 + threadIdx.x; k < ctas; k += 256)
-    if (recs[k].before == 2) atomicMin(&s_end, k);
+  if ((int)threadIdx.x > c && flag == 2) atomicMin(&s_end, (int)threadIdx.x);
   __syncthreads();
   const int l = threadIdx.x % L, g = threadIdx.x / L, end = s_end;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k = c + g; k <= end; k += G) {
-    if (k > c && recs[k].before == 0) continue;   // a CTA without work
+    if (k > c && s_flag[k] == 0) continue;   // a CTA without work
     const float4 x = reinterpret_cast<const float4*>(parts + ((int64_t)k * 2 + (k == c)) * HD)[l];
     s.x += x.x;
     s.y += x.y;
@@ -736,8 +835,6 @@ inline bool head_dim_supported(int dtype, int hd) {
   return dtype == HSTU_BF16 ? hd == 64 || hd == 128 : hd == 32 || hd == 64 || hd == 128;
 }
 
-// CTAs of the attention: one a SM, at most this many (the workspace holds a part record for each).
-constexpr int ATTN_MAX_CTAS = 256;
 inline size_t attention_workspace_bytes(int hd) {
   return (size_t)ATTN_MAX_CTAS * (2 * hd * sizeof(float) + sizeof(Part));
 }
@@ -752,7 +849,11 @@ hstu_status_t launch_attention_t(const Attn& a, void* ws, int sms, cudaStream_t 
   if (grid > ATTN_MAX_CTAS) grid = ATTN_MAX_CTAS;
   float* parts = static_cast<float*>(ws);
   Part* recs = reinterpret_cast<Part*>(parts + (size_t)ATTN_MAX_CTAS * 2 * HD);
-  attention_kernel<T, HD><<<(unsigned)grid, ATTN_THREADS, 0, st>>>(a, parts, recs);
+  auto kern = attention_kernel<T, HD>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem<HD>::TOTAL) !=
+      cudaSuccess)
+    return HSTU_ERR_CUDA;
+  kern<<<(unsigned)grid, ATTN_THREADS, AttnSmem<HD>::TOTAL, st>>>(a, parts, recs);
   hstu_status_t rc = launched();
   // one CTA joins its warps' parts itself, and a single tile a (sequence, head) has no parts
   if (rc != HSTU_OK || grid == 1 || a.max_len < TILE) return rc;
@@ -761,7 +862,7 @@ hstu_status_t launch_attention_t(const Attn& a, void* ws, int sms, cudaStream_t 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(ATTN_MAX_CTAS);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
