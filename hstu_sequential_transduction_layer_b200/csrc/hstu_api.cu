@@ -358,7 +358,9 @@ hstu_status_t check_cache(const hstu_paged_cache_t* c) {
     return HSTU_ERR_INVALID_ARG;
   if (!paged::head_dim_supported(c->dtype, c->head_dim)) return HSTU_ERR_UNSUPPORTED;
   if (4LL * c->num_heads * c->head_dim > (1LL << 30)) return HSTU_ERR_INVALID_ARG;
-  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return HSTU_ERR_INVALID_ARG;
+  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) || !aligned16(c->positions) ||
+      !aligned16(c->timestamps) || !aligned16(c->weights))
+    return HSTU_ERR_INVALID_ARG;
   return HSTU_OK;
 }
 
@@ -385,8 +387,8 @@ hstu_status_t check_table(int page_size, int64_t num_seqs, const int32_t* page_t
                           int64_t max_pages, const int64_t* cache_lens) {
   if (num_seqs < 0 || max_pages < 0 || max_pages >= (1LL << 31)) return HSTU_ERR_INVALID_ARG;
   if (num_seqs > 0 && (!page_table || !cache_lens || max_pages == 0)) return HSTU_ERR_INVALID_ARG;
-  // slots of a sequence are numbered in 32 bits
-  if (max_pages * page_size >= (1LL << 31)) return HSTU_ERR_UNSUPPORTED;
+  // slots of a sequence are numbered in 31 bits
+  if (max_pages * page_size >= (1LL << 30)) return HSTU_ERR_UNSUPPORTED;
   return HSTU_OK;
 }
 

@@ -100,37 +100,56 @@ template <> struct vec16<bf16> {
 // read from U|V|Q|K instead of a page, at distance 0.
 //
 // The unit of work is a tile of TILE rows of one (sequence, head): 4 KB of K and 4 KB of V.  All
-// tiles of the batch, in the order (sequence, head, tile), are dealt to the warps of a persistent
-// grid in equal contiguous ranges, so that one long history and many ragged ones load the SMs
-// alike; every CTA finds its ranges from the lengths itself (one block scan).  Each warp brings its
-// tiles into its own ring in shared memory by bulk copies.  A warp that holds all tiles of a
-// (sequence, head) writes its row of AV; parts are joined first among the CTA's warps in shared
-// memory, then, where a (sequence, head) spans CTAs, by a second kernel, always in the same order.
-constexpr int ATTN_WARPS = 12;
+// tiles of the batch, in the order (sequence, head, tile), are dealt to the consumer warps of a
+// persistent grid in equal contiguous ranges, so that one long history and many ragged ones load
+// the SMs alike; every CTA finds its ranges from the lengths itself (one block scan).  One producer
+// warp, a lane for each consumer warp, walks the ranges, looks the pages up and fills the warp's
+// ring in shared memory with K and V by bulk copies (as few as the pages allow: a copy occupies the
+// SM's copy engine for some 75 cycles, however small).  The consumer loads what else its tile needs
+// one tile ahead.  A warp that holds all tiles of a (sequence, head) writes its row of AV; parts
+// are joined first among the CTA's warps in shared memory, then, where a (sequence, head) spans
+// CTAs, by a second kernel, always in the same order.
+constexpr int ATTN_WARPS = 12;                  // consumers
 constexpr int ATTN_STAGES = 2;
-constexpr int ATTN_THREADS = ATTN_WARPS * 32;
+constexpr int ATTN_THREADS = (ATTN_WARPS + 1) * 32;
 constexpr int ATTN_HALF = 4096;                 // bytes of a tile's K, and of its V
-template <int HD> struct AttnSmem {
-  static constexpr int RING = ATTN_WARPS * ATTN_STAGES * 2 * ATTN_HALF;
-  static constexpr int PARTS = ATTN_WARPS * 2 * HD * 4;
-  static constexpr int TOTAL = RING + PARTS + 128;   // + alignment
-};
-
 // CTAs of the attention: one a SM, at most this many (the workspace holds a part record for each).
 constexpr int ATTN_MAX_CTAS = 256;
+
+// What a consumer is told of a tile: written by the producer beside the rows.
+struct __align__(16) TileInfo {
+  int32_t pair, b, h;      // sequence * H + head, and both
+  int32_t first;           // the tile's first slot
+  int32_t left;            // cached rows from the tile's first on; below TILE: its last tile
+  int32_t flags;           // bit 0: the first tile; bit 1 + p: 16-row piece p has no page
+  int32_t p_new;           // the new token's position and time
+  int64_t t_new;
+  int64_t row[2];          // rows of the pieces in K, V and weights: (page * H + h) * page_size + offset
+  int64_t slot[2];         // and in positions and times: page * page_size + offset
+  int64_t to;              // where the new token's row goes, or -1
+  int64_t to_slot;         // its slot (page * page_size + offset) for position and time, or -1
+};
+
+template <typename T, int HD>
+struct AttnCfg {
+  static constexpr int E = vec16<T>::N;      // elements a lane holds of a row
+  static constexpr int LPR = HD / E;         // lanes a row
+  static constexpr int RPI = 32 / LPR;       // rows a warp-wide load
+  static constexpr int TILE = 8 * RPI;
+  static constexpr int NP = TILE > 16 ? TILE / 16 : 1;
+  static constexpr int PIECE = TILE / NP;    // rows a piece: pieces do not cross pages
+  static constexpr int ROW = HD * (int)sizeof(T);
+  static constexpr int STAGE = 2 * ATTN_HALF;   // K and V
+  static constexpr int RING = ATTN_WARPS * ATTN_STAGES * STAGE;
+  static constexpr int SMEM = RING + ATTN_WARPS * 2 * HD * 4 + 128;   // + alignment
+  static_assert(LPR >= 8 && LPR <= 32, "a row spans 8 to 32 lanes");
+  static_assert(TILE * ROW == ATTN_HALF && NP <= 2, "a tile is 4 KB of K");
+};
 
 // What a CTA leaves for the joining kernel.
 struct Part {
   int32_t pair;     // sequence * H + head of the part that goes on in the next CTA, or -1
   int32_t before;   // 0: no part that began in an earlier CTA; 1: one that goes on; 2: one that ends here
-};
-
-// One tile: sequence, head, tile index, the sequence's cached length and tiles a head, and the
-// pages of the tile's 16-row pieces (-1: none).
-template <int NP>
-struct Tile {
-  int b, h, i, n, tiles;
-  int pg[NP];
 };
 
 // Copies `bytes` (a multiple of 16, both addresses 16-byte aligned) and counts them on `bar`.
@@ -142,47 +161,56 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// a / b for 0 <= a, 0 < b; the 64-bit division takes several times as long as the 32-bit one.
-__device__ __forceinline__ int64_t div_by(int64_t a, int b) {
-  return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(sm100::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a, float* parts, Part* recs) {
-  using sm100::f2_add;
   using sm100::f2_fma;
   using sm100::f2_pack;
   using sm100::f2_unpack;
-  constexpr int E = vec16<T>::N;      // elements a lane holds of a row
-  constexpr int LPR = HD / E;         // lanes a row
-  constexpr int RPI = 32 / LPR;       // rows a warp-wide load
-  constexpr int TILE = 8 * RPI;
-  constexpr int NP = TILE > 16 ? TILE / 16 : 1;
-  constexpr int PIECE = TILE / NP;    // rows a piece
-  constexpr int ROW = HD * (int)sizeof(T);
-  static_assert(LPR >= 8 && LPR <= 32, "a row spans 8 to 32 lanes");
-  static_assert(TILE * ROW == ATTN_HALF, "a tile is 4 KB of K");
+  using Cfg = AttnCfg<T, HD>;
+  constexpr int E = Cfg::E, LPR = Cfg::LPR, RPI = Cfg::RPI, TILE = Cfg::TILE, NP = Cfg::NP,
+                PIECE = Cfg::PIECE, ROW = Cfg::ROW, STAGE = Cfg::STAGE;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((128 - (sm100::smem_u32(smem_raw) & 127)) & 127);
-  float(*sp)[2][HD] = reinterpret_cast<float(*)[2][HD]>(smem + AttnSmem<HD>::RING);
-  __shared__ int64_t pre[ATTN_THREADS];
-  __shared__ int s_len[ATTN_THREADS];
-  __shared__ int64_t scratch[ATTN_WARPS];
+  float(*sp)[2][HD] = reinterpret_cast<float(*)[2][HD]>(smem + Cfg::RING);
+  __shared__ int pre[ATTN_THREADS], s_len[ATTN_THREADS];
+  __shared__ int scratch[ATTN_WARPS + 1];
   __shared__ int s_before[ATTN_WARPS], s_pair[ATTN_WARPS];
-  __shared__ __align__(8) uint64_t bars[ATTN_WARPS][ATTN_STAGES];
+  __shared__ TileInfo s_info[ATTN_WARPS][ATTN_STAGES];
+  __shared__ int s_issued[ATTN_WARPS];   // tiles whose TileInfo is written
+  __shared__ __align__(8) uint64_t full_bar[ATTN_WARPS][ATTN_STAGES], free_bar[ATTN_WARPS][ATTN_STAGES];
   __shared__ int s_abort;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int sub = lane % LPR, grp = lane / LPR;
   const int H = a.c.H, shift = a.c.ps_shift, ps = 1 << shift, B = (int)a.B;
   const int64_t room = (a.max_pages << shift) - (a.append ? 1 : 0);
   const int64_t most = a.max_len < room ? a.max_len : room;
+  // a sequence's cached length, doubled, plus 1 where it was clamped (its token is not stored)
+  auto coded_len = [&](int b) {
+    const int64_t len = a.lens[b], n = cached_len(len, most);
+    return n < 0 ? -1 : (int)(2 * n + (n != len));
+  };
   auto tiles_of = [&](int n) { return n < 0 ? 0 : n / TILE + 1; };   // of n cached rows and the new one
 
-  if (lane == 0) {
+  if (warp < ATTN_WARPS && lane == 0) {
     s_before[warp] = 0;
+    s_issued[warp] = 0;
     s_pair[warp] = -1;
 #pragma unroll
-    for (int k = 0; k < ATTN_STAGES; k++) sm100::mbar_init(&bars[warp][k], 1);
+    for (int k = 0; k < ATTN_STAGES; k++) {
+      sm100::mbar_init(&full_bar[warp][k], 1);
+      sm100::mbar_init(&free_bar[warp][k], 1);
+    }
     sm100::fence_mbar_init();
   }
   if (threadIdx.x == 0) {
@@ -191,208 +219,259 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
   }
   // tiles a head up to each group of C sequences; with C = 1 the lengths stay in shared memory
   const int C = (B + ATTN_THREADS - 1) / ATTN_THREADS;
-  int64_t sum = 0;
-  int n_one = -1;
-  for (int b = threadIdx.x * C; b < B && b < (threadIdx.x + 1) * C; b++) {
-    n_one = (int)cached_len(a.lens[b], most);
-    sum += tiles_of(n_one);
-  }
-  s_len[threadIdx.x] = n_one;
   {
-    int64_t x = sum;
+    int x = 0, code = -1;
+    for (int b = threadIdx.x * C; b < B && b < (int)(threadIdx.x + 1) * C; b++) {
+      code = coded_len(b);
+      x += tiles_of(code >> 1);
+    }
+    s_len[threadIdx.x] = code;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
-    int64_t before = 0;
 #pragma unroll
-    for (int w = 0; w < ATTN_WARPS; w++) before += w < warp ? scratch[w] : 0;
-    pre[threadIdx.x] = x + before;
+    for (int w = 0; w < ATTN_WARPS; w++) x += w < warp ? scratch[w] : 0;
+    pre[threadIdx.x] = x;
     __syncthreads();
   }
-  auto length = [&](int b) { return C == 1 ? s_len[b] : (int)cached_len(a.lens[b], most); };
-  // every warp's share: `share` tiles, one more for the first `over` warps
-  const int64_t units = pre[ATTN_THREADS - 1] * H;
-  const int gw = blockIdx.x * ATTN_WARPS + warp, W = gridDim.x * ATTN_WARPS;
-  const int64_t share = div_by(units, W);
-  const int over = (int)(units - share * W);
-  const int64_t u0 = gw * share + (gw < over ? gw : over), u1 = u0 + share + (gw < over ? 1 : 0);
+  // every consumer's share: `share` tiles, one more for the first `over` of them
+  const uint32_t units = (uint32_t)pre[ATTN_THREADS - 1] * H, W = gridDim.x * ATTN_WARPS;
+  const uint32_t share = units / W, over = units - share * W;
 
-  if (u0 < u1) {
-    using Tl = Tile<NP>;
-    auto pages = [&](Tl& t) {
-      const int32_t* row = a.table + (int64_t)t.b * a.max_pages;
+  int done = 0;   // tiles taken
+  if (warp == ATTN_WARPS) {
+    const uint32_t gw = blockIdx.x * ATTN_WARPS + lane;
+    const uint32_t u0 = gw * share + (gw < over ? gw : over);
+    const int count = lane < ATTN_WARPS ? (int)(share + (gw < over ? 1 : 0)) : 0;
+    int b = 0, h = 0, i = 0, n = 0, code = 0, tiles = 1;
+    int32_t pg[NP];
+    auto length = [&](int s) { return C == 1 ? s_len[s] : coded_len(s); };
+    // the pages of the tile's pieces, that of the new token's row among them
+    auto pages = [&]() {
+      const int32_t* row = a.table + (int64_t)b * a.max_pages;
 #pragma unroll
       for (int p = 0; p < NP; p++) {
-        const int j = t.i * TILE + PIECE * p;
-        t.pg[p] = j < t.n ? (int)page_of(row, j >> shift, a.c.num_pages) : -1;
+        const int j = i * TILE + PIECE * p;
+        pg[p] = j < n + a.append ? row[j >> shift] : -1;
       }
     };
-    // the first unit: its group by comparing every ATTN_WARPS-th sum, then the sums between, and
-    // with more than one sequence a group by scans over 32 lengths at a time
-    Tl cur;
-    {
-      const int64_t v = div_by(u0, H);
-      const unsigned c1 = __ballot_sync(0xffffffffu, pre[lane * ATTN_WARPS + ATTN_WARPS - 1] > v);
-      const int g = c1 ? __ffs(c1) - 1 : 31;
-      const unsigned c2 = __ballot_sync(0xffffffffu, lane < ATTN_WARPS && pre[g * ATTN_WARPS + lane % ATTN_WARPS] > v);
-      const int lo = g * ATTN_WARPS + (c2 ? __ffs(c2) - 1 : ATTN_WARPS - 1);
-      int64_t base = lo ? pre[lo - 1] : 0;
-      cur.b = lo < B ? lo : B - 1;
-      if (C > 1) {
-        int b0 = lo * C;
-        cur.b = B - 1;
-        while (b0 < B) {   // ends with a hit: v is below the batch's tiles
-          const int b = b0 + lane;
-          const int t = b < B ? tiles_of(length(b)) : 0;
-          int64_t x = t;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-          }
-          const unsigned hit = __ballot_sync(0xffffffffu, base + x > v);
-          if (hit) {
-            const int f = __ffs(hit) - 1;
-            cur.b = b0 + f;
-            base += __shfl_sync(0xffffffffu, x - t, f);
-            break;
-          }
-          base += __shfl_sync(0xffffffffu, x, 31);
-          b0 += 32;
-        }
+    if (count > 0) {
+      // the range's first tile: the first group whose running sum exceeds v, and the sequence in it
+      const int v = (int)(u0 / (uint32_t)H);
+      int lo = 0, hi = B < ATTN_THREADS ? B - 1 : ATTN_THREADS - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (pre[mid] > v) hi = mid; else lo = mid + 1;
       }
-      cur.n = length(cur.b);
-      cur.tiles = cur.n < 0 ? 1 : tiles_of(cur.n);
-      const int64_t r = u0 - base * H;
-      cur.h = (int)div_by(r, cur.tiles);
-      cur.i = (int)(r - (int64_t)cur.h * cur.tiles);
+      int base = lo ? pre[lo - 1] : 0;
+      b = lo * C;
+      code = length(b);
+      while (base + tiles_of(code >> 1) <= v && b + 1 < B) {
+        base += tiles_of(code >> 1);
+        code = length(++b);
+      }
+      n = code >> 1;
+      tiles = n < 0 ? 1 : tiles_of(n);
+      const uint32_t r = u0 - (uint32_t)base * H;
+      h = (int)(r / (uint32_t)tiles);
+      i = (int)(r - (uint32_t)h * tiles);
+      pages();
     }
-    auto advance = [&](Tl& t) {
-      if (++t.i == t.tiles) {
-        t.i = 0;
-        if (++t.h == H) {
-          t.h = 0;
-          t.n = -1;
-          while (t.n < 0 && t.b + 1 < B) t.n = length(++t.b);
-          t.tiles = tiles_of(t.n);
+    int p_new = 0, owner = -1;
+    int64_t t_new = 0;
+    uint64_t idle = 0;
+    while (__any_sync(0xffffffffu, done < count)) {
+      const int stage = done % ATTN_STAGES;
+      const bool go = done < count && (done < ATTN_STAGES ||
+                                       mbar_test(&free_bar[lane][stage], (done / ATTN_STAGES + 1) & 1));
+      if (go) {
+        if (owner != b) {
+          owner = b;
+          const int64_t p = a.next_pos ? a.next_pos[b] : n;
+          if (p < 0 || p > 0x7fffffff) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
+          p_new = p < 0 ? 0 : (p > 0x7fffffff ? 0x7fffffff : (int)p);
+          t_new = a.now ? a.now[b] : 0;
         }
-      }
-    };
-    auto u_row = [&](const Tl& t, int block) {   // the new token's U, V, Q or K of the head
-      return static_cast<const T*>(a.uvqk) + (((int64_t)t.b * 4 + block) * H + t.h) * HD;
-    };
-    unsigned char* ring = smem + warp * (ATTN_STAGES * 2 * ATTN_HALF);
-    // the tile's K and V rows, piece by piece, and the new token's into the row after the last
-    auto issue = [&](const Tl& t, int stage) {
-      if (lane == 0) {
-        uint64_t* bar = &bars[warp][stage];
-        unsigned char* dst = ring + stage * 2 * ATTN_HALF;
-        int rows[NP], total = 0;
+        uint64_t* bar = &full_bar[lane][stage];
+        unsigned char* dst = smem + (lane * ATTN_STAGES + stage) * STAGE;
+        TileInfo info;
+        info.pair = b * H + h;
+        info.b = b;
+        info.h = h;
+        info.first = i * TILE;
+        info.left = n - i * TILE;
+        info.flags = i == 0;
+        info.p_new = p_new;
+        info.t_new = t_new;
+        info.to = info.to_slot = -1;
+        int rows[NP], sum = 0;
 #pragma unroll
         for (int p = 0; p < NP; p++) {
-          const int left = t.n - (t.i * TILE + PIECE * p);
-          rows[p] = t.pg[p] < 0 || left <= 0 ? 0 : (left < PIECE ? left : PIECE);
-          total += rows[p];
+          const int left = info.left - PIECE * p, at = (i * TILE + PIECE * p) & (ps - 1);
+          rows[p] = left <= 0 ? 0 : (left < PIECE ? left : PIECE);
+          if ((uint32_t)pg[p] >= (uint32_t)a.c.num_pages) {
+            if (left + a.append > 0) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
+            info.flags |= 2 << p;
+            rows[p] = 0;
+          }
+          info.slot[p] = ((int64_t)pg[p] << shift) + at;
+          info.row[p] = (((int64_t)pg[p] * H + h) << shift) + at;
+          sum += rows[p];
+          if (a.append && left >= 0 && left < PIECE && !(code & 1) && !(info.flags & (2 << p))) {
+            info.to = info.row[p] + left;
+            if (h == 0) info.to_slot = info.slot[p] + left;
+          }
         }
-        const bool own = t.i == t.tiles - 1;
-        sm100::mbar_arrive_expect_tx(bar, (uint32_t)(total + own) * 2 * ROW);
+        s_info[lane][stage] = info;
+        __threadfence_block();
+        *reinterpret_cast<volatile int*>(&s_issued[lane]) = done + 1;
+        sm100::mbar_arrive_expect_tx(bar, (uint32_t)sum * 2 * ROW);
+        if (NP > 1 && ps >= TILE) {   // one page
+          rows[0] = sum;
+          rows[NP - 1] = 0;
+        }
 #pragma unroll
         for (int p = 0; p < NP; p++) {
           if (rows[p] == 0) continue;
-          const int64_t at = ((((int64_t)t.pg[p] * H + t.h) << shift) + ((t.i * TILE + PIECE * p) & (ps - 1))) * HD;
+          const int64_t at = info.row[p] * HD;
           bulk_load(dst + p * PIECE * ROW, static_cast<const T*>(a.c.k) + at, rows[p] * ROW, bar);
           bulk_load(dst + ATTN_HALF + p * PIECE * ROW, static_cast<const T*>(a.c.v) + at, rows[p] * ROW, bar);
         }
-        if (own) {
-          const int o = (t.n - t.i * TILE) * ROW;
-          bulk_load(dst + o, u_row(t, 3), ROW, bar);
-          bulk_load(dst + ATTN_HALF + o, u_row(t, 1), ROW, bar);
+        if (++done < count) {
+          if (++i == tiles) {
+            i = 0;
+            if (++h == H) {
+              h = 0;
+              code = -1;
+              while (code < 0 && b + 1 < B) code = length(++b);
+              n = code >> 1;
+              tiles = tiles_of(n);
+            }
+          }
+          pages();
+        }
+        idle = 0;
+      } else if (done < count) {
+        // nothing to refill yet: bounded, as every wait of this kernel
+        const uint64_t now = sm100::globaltimer();
+        if (idle == 0) idle = now;
+        if (now - idle > 2 * sm100::kWaitLimitNs) {
+          s_abort = 1;
+          report(HSTU_ERR_DEVICE_TIMEOUT);
         }
       }
-    };
-    // What the lane needs for the row of a tile that is its own after the exchange of partial sums
-    // comes in two steps: position, time and weight two tiles ahead (they need the page), the
-    // biases they select one tile ahead.
-    const int mine = (sub % 8) * RPI + grp;
-    struct Raw {
+      if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort))) break;
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else {
+    const int gw = blockIdx.x * ATTN_WARPS + warp;
+    const int count = (int)(share + ((uint32_t)gw < over ? 1 : 0));
+    const int sub = lane % LPR, grp = lane / LPR;
+    const int mine = (sub % 8) * RPI + grp;   // the lane's own row after the exchange of partial sums
+    // What a tile needs besides K and V, loaded while the tile before is worked on: the lane's own
+    // row's position, time and weight, and with the first tile the lane's piece of Q.  (The new
+    // token's K and V are loaded with the last tile.)
+    struct Ahead {
       int p;
       float w;
       int64_t t;
     };
-    struct Own {
-      float bias, w;
+    uint4 q, k_own, v_own, q_next;
+    q = k_own = v_own = q_next = make_uint4(0, 0, 0, 0);
+    auto on_page = [&](const TileInfo& t) {   // the lane's own row is cached
+      return mine < t.left && !(t.flags & (NP > 1 && mine >= PIECE ? 4 : 2));
     };
-    auto own_page = [&](const Tl& t) { return NP > 1 && mine >= 16 ? t.pg[NP - 1] : t.pg[0]; };
-    int p_new = 0;         // position and time of the new token of the tile last looked up
-    int64_t t_new = 0;
-    auto load_raw = [&](const Tl& t, bool fresh) {
-      if (fresh) {
-        const int64_t p = a.next_pos ? a.next_pos[t.b] : t.n;
-        if (p < 0 || p > 0x7fffffff) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
-        p_new = p < 0 ? 0 : (p > 0x7fffffff ? 0x7fffffff : (int)p);
-        t_new = a.now ? a.now[t.b] : 0;
+    auto place = [&](const int64_t* at) { return (NP > 1 && mine >= PIECE ? at[1] - PIECE : at[0]) + mine; };
+    auto look_ahead = [&](const TileInfo& t, bool fresh) {
+      Ahead r{t.first + mine, 0.0f, 0};
+      if (on_page(t)) {
+        const int64_t slot = place(t.slot);
+        if (a.c.positions && (a.pos || a.alibi)) r.p = a.c.positions[slot];
+        if (a.tim) r.t = a.c.timestamps[slot];
+        if (a.c.weights) r.w = a.c.weights[place(t.row)];
+      } else {   // the new token's own row is at distance 0
+        r.p = t.p_new;
+        r.t = t.t_new;
       }
-      const int j = t.i * TILE + mine, pg = own_page(t);
-      Raw m{j, 0.0f, 0};
-      if (j < t.n && pg >= 0) {
-        const int64_t s = ((int64_t)pg << shift) + (j & (ps - 1));
-        if (a.c.positions && (a.pos || a.alibi)) m.p = a.c.positions[s];
-        if (a.tim) m.t = a.c.timestamps[s];
-        if (a.c.weights) m.w = a.c.weights[(((int64_t)pg * H + t.h) << shift) + (j & (ps - 1))];
-      } else {
-        m.p = p_new;
-        m.t = t_new;
-      }
-      return m;
-    };
-    auto look_up = [&](const Tl& t, const Raw& m) {
-      Own r{0.0f, m.w};
-      const int far = p_new - m.p, dist = far < 0 ? 0 : far;
-      if (a.pos) r.bias = a.pos[(int64_t)t.h * a.P + (dist < a.P ? dist : a.P - 1)];
-      if (a.tim) r.bias += a.tim[(int64_t)t.h * a.Tb + time_bucket(t_new - m.t, a.Tb)];
-      if (a.alibi) r.bias = -a.alibi[t.h] * (float)dist;
+      const T* u = static_cast<const T*>(a.uvqk) + ((int64_t)t.b * 4 * H + t.h) * HD + sub * E;
+      if (fresh) q_next = *reinterpret_cast<const uint4*>(u + 2LL * H * HD);
       return r;
     };
-    auto load_query = [&](const Tl& t) {
-      return *reinterpret_cast<const uint4*>(u_row(t, 2) + sub * E);
+    auto bias_of = [&](const TileInfo& t, const Ahead& r) {
+      float x = 0.0f;
+      const int far = t.p_new - r.p, dist = far < 0 ? 0 : far;
+      if (a.pos) x = a.pos[(int64_t)t.h * a.P + (dist < a.P ? dist : a.P - 1)];
+      else if (a.alibi) x = -a.alibi[t.h] * (float)dist;
+      if (a.tim) x += a.tim[(int64_t)t.h * a.Tb + time_bucket(t.t_new - r.t, a.Tb)];
+      return x;
     };
-    // nxt: the tile after cur, in flight; far: the one after that, its pages being looked up
-    Tl nxt = cur, far;
-    if (u0 + 1 < u1) advance(nxt);
-    far = nxt;
-    if (u0 + 2 < u1) advance(far);
-    pages(cur);
-    pages(nxt);
-    pages(far);
-    uint4 query = load_query(cur);
-    __syncwarp();
-    issue(cur, 0);
-    if (u0 + 1 < u1) issue(nxt, 1);
-    Raw raw = load_raw(cur, true);
-    Own own = look_up(cur, raw);
-    if (u0 + 1 < u1) raw = load_raw(nxt, nxt.i == 0);
+    auto issued = [&](int k) {
+      const bool is = *reinterpret_cast<volatile int*>(&s_issued[warp]) > k;
+      __threadfence_block();
+      return __all_sync(0xffffffffu, is);
+    };
+    auto await = [&](int k) {   // bounded, as every wait of this kernel
+      const uint64_t t0 = sm100::globaltimer();
+      while (!issued(k)) {
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort))) return false;
+        if (__any_sync(0xffffffffu, sm100::globaltimer() - t0 > sm100::kWaitLimitNs)) {
+          if (lane == 0) {
+            s_abort = 1;
+            report(HSTU_ERR_DEVICE_TIMEOUT);
+          }
+          return false;
+        }
+      }
+      return true;
+    };
     uint64_t acc[E / 2];
 #pragma unroll
     for (int e = 0; e < E / 2; e++) acc[e] = 0;
-    bool whole = cur.i == 0;   // acc holds the (sequence, head) from its first tile on
-    int stage = 0, parity = 0;
-    bool ok = true;
-    for (int64_t u = u0; u < u1; u++) {
-      const bool more = u + 1 < u1;
-      const uint4 y = query;
-      if (more && nxt.i == 0) query = load_query(nxt);
-      const bool full = (cur.i + 1) * TILE <= cur.n && cur.pg[0] >= 0 && cur.pg[NP - 1] >= 0;
-      const uint4* ks = reinterpret_cast<const uint4*>(ring + stage * 2 * ATTN_HALF) + lane;
+    bool whole = true, ok = true;   // whole: acc holds the (sequence, head) from its first tile on
+    float bias = 0.0f, weight = 0.0f;
+    if (count > 0 && (ok = await(0))) {
+      const TileInfo& t = s_info[warp][0];
+      whole = t.flags & 1;
+      const Ahead r = look_ahead(t, true);
+      q = q_next;
+      bias = bias_of(t, r);
+      weight = r.w;
+    }
+    for (; ok && done < count; done++) {
+      const int stage = done % ATTN_STAGES;
+      const TileInfo &info = s_info[warp][stage], &next = s_info[warp][(done + 1) % ATTN_STAGES];
+      unsigned char* src = smem + (warp * ATTN_STAGES + stage) * STAGE;
+      const int left = info.left, flags = info.flags, pair = info.pair;
+      const bool more = done + 1 < count, early = more && issued(done + 1);
+      const bool last = left < TILE;
+      Ahead ahead;
+      if (early) ahead = look_ahead(next, next.flags & 1);
+      if (last) {
+        const T* u = static_cast<const T*>(a.uvqk) + ((int64_t)info.b * 4 * H + info.h) * HD + sub * E;
+        k_own = *reinterpret_cast<const uint4*>(u + 3LL * H * HD);
+        v_own = *reinterpret_cast<const uint4*>(u + (int64_t)H * HD);
+      }
+      ok = sm100::mbar_wait(&full_bar[warp][stage], (done / ATTN_STAGES) & 1, &s_abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint4* ks = reinterpret_cast<const uint4*>(src) + lane;
       const uint4* vs = ks + ATTN_HALF / 16;
-      ok = sm100::mbar_wait(&bars[warp][stage], parity, &s_abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (last) {
+        // the new token's rows go behind the last cached ones
+        if (grp == 0) {
+          *reinterpret_cast<uint4*>(src + left * ROW + sub * 16) = k_own;
+          *reinterpret_cast<uint4*>(src + ATTN_HALF + left * ROW + sub * 16) = v_own;
+        }
+        __syncwarp();
+      }
+      const bool cached = on_page(info);
       uint64_t f[E / 2], qf[E / 2];
       float part[8];
-      vec16<T>::widen(y, qf);
+      vec16<T>::widen(q, qf);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         vec16<T>::widen(ks[i * 32], f);
@@ -416,58 +495,50 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
       }
 #pragma unroll
       for (int w = 8; w < LPR; w <<= 1) part[0] += __shfl_xor_sync(0xffffffffu, part[0], w);
-      const int j = cur.i * TILE + mine, pg = own_page(cur);
       float wgt = 0.0f;
-      if (j == cur.n || (j < cur.n && pg >= 0)) {
-        const float x = part[0] + own.bias;
-        wgt = a.scale * silu_accurate(x);
-        if (a.c.weights && j < cur.n && sub < 8)
-          a.c.weights[(((int64_t)pg * H + cur.h) << shift) + (j & (ps - 1))] = own.w + fabsf(wgt);
+      if (cached || mine == left) {
+        wgt = a.scale * silu_accurate(part[0] + bias);
+        if (a.c.weights && cached && sub < 8) a.c.weights[place(info.row)] = weight + fabsf(wgt);
       }
-      if (more) own = look_up(nxt, raw);
+      if (early) {
+        bias = bias_of(next, ahead);
+        weight = ahead.w;
+      }
+      const bool full = left >= TILE && !(flags & ~1);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const float w = __shfl_sync(0xffffffffu, wgt, grp * LPR + i);
         uint4 r = vs[i * 32];
         if (!full) {
           // rows past the new token's, or of no page, hold what was there before
-          const int jr = cur.i * TILE + i * RPI + grp;
-          if (jr > cur.n || (jr < cur.n && cur.pg[i * RPI / 16] < 0)) r = make_uint4(0, 0, 0, 0);
+          const int row = i * RPI + grp;
+          if (row > left || (row < left && (flags & (2 << (i * RPI / 16))))) r = make_uint4(0, 0, 0, 0);
         }
         vec16<T>::widen(r, f);
         const uint64_t ww = f2_pack(w, w);
 #pragma unroll
         for (int e = 0; e < E / 2; e++) acc[e] = f2_fma(ww, f[e], acc[e]);
       }
-      const bool last = cur.i == cur.tiles - 1;
-      if (last && a.append && a.lens[cur.b] == cur.n && cur.n <= room) {
-        // the new row joins the cache: one row piece's lanes copy K and V, the lane that owns the
-        // row writes its weight and, for head 0, position and time
-        const int64_t to = page_of(a.table + (int64_t)cur.b * a.max_pages, cur.n >> shift, a.c.num_pages);
-        const int64_t o = cur.n & (ps - 1);
-        if (to >= 0) {
-          const int64_t r = ((to * H + cur.h) << shift) + o;
-          if (grp == 0) {
-            const int at = (cur.n - cur.i * TILE) * LPR + sub - lane;
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.c.k) + r * HD + sub * E) = ks[at];
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.c.v) + r * HD + sub * E) = vs[at];
-          }
-          if (j == cur.n && sub < 8) {
-            if (a.c.weights) a.c.weights[r] = fabsf(wgt);
-            if (cur.h == 0) {
-              if (a.c.positions)
-                a.c.positions[(to << shift) + o] = (int32_t)(a.next_pos ? a.next_pos[cur.b] : cur.n);
-              if (a.c.timestamps && a.now) a.c.timestamps[(to << shift) + o] = a.now[cur.b];
-            }
+      if (last && info.to >= 0) {
+        // the new row joins the cache: one group's lanes copy K and V, the lane that owns the row
+        // writes its weight and, for head 0, position and time
+        if (grp == 0) {
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.c.k) + info.to * HD + sub * E) = k_own;
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.c.v) + info.to * HD + sub * E) = v_own;
+        }
+        if (mine == left && sub < 8) {
+          if (a.c.weights) a.c.weights[info.to] = fabsf(wgt);
+          if (info.to_slot >= 0) {
+            if (a.c.positions) a.c.positions[info.to_slot] = info.p_new;
+            if (a.c.timestamps && a.now) a.c.timestamps[info.to_slot] = info.t_new;
           }
         }
       }
+      if (last)   // rows written here come before the copies that will refill the stage
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();   // every lane has read the stage
-      if (u + 2 < u1) {
-        issue(far, stage);
-        raw = load_raw(far, far.i == 0);
-      }
-      if (last || !more) {
+      if (lane == 0) sm100::mbar_arrive(&free_bar[warp][stage]);
+      if (last || done + 1 == count) {
         float s[E];
 #pragma unroll
         for (int e = 0; e < E / 2; e++) f2_unpack(acc[e], s[2 * e], s[2 * e + 1]);
@@ -475,7 +546,6 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
         for (int w = LPR; w < 32; w <<= 1)
 #pragma unroll
           for (int e = 0; e < E; e++) s[e] += __shfl_xor_sync(0xffffffffu, s[e], w);
-        const int pair = cur.b * H + cur.h;
         float* to = last && whole ? a.av + (int64_t)pair * HD : sp[warp][whole];
         if (grp == 0) {
 #pragma unroll
@@ -490,27 +560,30 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
         for (int e = 0; e < E / 2; e++) acc[e] = 0;
         whole = true;
       }
-      cur = nxt;
-      nxt = far;
-      if (u + 3 < u1) {
-        advance(far);
-        pages(far);
+      if (more && !early) {
+        ok = await(done + 1);
+        if (ok) {
+          const Ahead r = look_ahead(next, next.flags & 1);
+          bias = bias_of(next, r);
+          weight = r.w;
+        }
       }
-      stage ^= 1;
-      parity ^= stage == 0;
-    }
-    if (!__all_sync(0xffffffffu, ok)) {
-      // gave up: what is still being copied lands before the CTA goes
-      sm100::mbar_drain(&bars[warp][stage], parity);
-      sm100::mbar_drain(&bars[warp][stage ^ 1], parity ^ (stage == 1));
+      q = q_next;
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // rows of inactive sequences
   for (int b = blockIdx.x; b < B; b += gridDim.x)
-    if (length(b) < 0)
+    if ((C == 1 ? s_len[b] : coded_len(b)) < 0)
       for (int i = threadIdx.x; i < H * HD; i += ATTN_THREADS) a.av[(int64_t)b * H * HD + i] = 0.0f;
   __syncthreads();
+  if (s_abort) {
+    // gave up: what is still being copied lands before the CTA goes
+    if (warp < ATTN_WARPS && lane == 0)
+      for (int k = done; k < done + ATTN_STAGES; k++)
+        sm100::mbar_drain(&full_bar[warp][k % ATTN_STAGES], (k / ATTN_STAGES) & 1);
+    return;
+  }
+  if (warp == ATTN_WARPS) return;
   // A warp's open end is followed by the later warps' parts, up to the one that ends it.  Parts that
   // began in an earlier CTA come before the first open end.
   const int flag = lane < ATTN_WARPS ? s_before[lane] : 0;
@@ -841,19 +914,20 @@ inline size_t attention_workspace_bytes(int hd) {
 
 template <typename T, int HD>
 hstu_status_t launch_attention_t(const Attn& a, void* ws, int sms, cudaStream_t st) {
-  constexpr int TILE = 8 * 32 * vec16<T>::N / HD;
-  // no more CTAs than give each warp one tile of the longest announced length
+  constexpr int TILE = AttnCfg<T, HD>::TILE, SMEM = AttnCfg<T, HD>::SMEM;
+  // no more CTAs than give each warp one tile of the longest announced length; tiles are counted
+  // in 32 bits
   const int64_t tiles = a.B * a.c.H * (a.max_len / TILE + 1);
+  if (a.max_len >= (1LL << 30) || tiles >= (1LL << 31)) return HSTU_ERR_UNSUPPORTED;
   int64_t grid = (tiles + ATTN_WARPS - 1) / ATTN_WARPS;
   if (grid > sms) grid = sms;
   if (grid > ATTN_MAX_CTAS) grid = ATTN_MAX_CTAS;
   float* parts = static_cast<float*>(ws);
   Part* recs = reinterpret_cast<Part*>(parts + (size_t)ATTN_MAX_CTAS * 2 * HD);
   auto kern = attention_kernel<T, HD>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem<HD>::TOTAL) !=
-      cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
     return HSTU_ERR_CUDA;
-  kern<<<(unsigned)grid, ATTN_THREADS, AttnSmem<HD>::TOTAL, st>>>(a, parts, recs);
+  kern<<<(unsigned)grid, ATTN_THREADS, SMEM, st>>>(a, parts, recs);
   hstu_status_t rc = launched();
   // one CTA joins its warps' parts itself, and a single tile a (sequence, head) has no parts
   if (rc != HSTU_OK || grid == 1 || a.max_len < TILE) return rc;
