@@ -111,6 +111,7 @@ template <> struct vec16<bf16> {
 // CTAs, by a second kernel, always in the same order.
 constexpr int ATTN_WARPS = 12;                  // consumers
 constexpr int ATTN_STAGES = 2;
+constexpr int ATTN_INFOS = 4;                   // tiles told of: two in flight and two ahead
 constexpr int ATTN_THREADS = (ATTN_WARPS + 1) * 32;
 constexpr int ATTN_HALF = 4096;                 // bytes of a tile's K, and of its V
 // CTAs of the attention: one a SM, at most this many (the workspace holds a part record for each).
@@ -141,7 +142,8 @@ struct AttnCfg {
   static constexpr int ROW = HD * (int)sizeof(T);
   static constexpr int STAGE = 2 * ATTN_HALF;   // K and V
   static constexpr int RING = ATTN_WARPS * ATTN_STAGES * STAGE;
-  static constexpr int SMEM = RING + ATTN_WARPS * 2 * HD * 4 + 128;   // + alignment
+  static constexpr int PARTS = RING, ROWS = PARTS + ATTN_WARPS * 2 * HD * 4;
+  static constexpr int SMEM = ROWS + ATTN_WARPS * 2 * 32 * 16 + 128;   // + alignment
   static_assert(LPR >= 8 && LPR <= 32, "a row spans 8 to 32 lanes");
   static_assert(TILE * ROW == ATTN_HALF && NP <= 2, "a tile is 4 KB of K");
 };
@@ -159,6 +161,20 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
           sm100::smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar))
       : "memory");
+}
+
+// Copies 4 or 8 bytes for the calling thread, in its current group.
+template <int N>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "n"(N)
+               : "memory");
+}
+
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of the calling thread's groups are in flight.
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
@@ -183,11 +199,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
                 PIECE = Cfg::PIECE, ROW = Cfg::ROW, STAGE = Cfg::STAGE;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((128 - (sm100::smem_u32(smem_raw) & 127)) & 127);
-  float(*sp)[2][HD] = reinterpret_cast<float(*)[2][HD]>(smem + Cfg::RING);
+  float(*sp)[2][HD] = reinterpret_cast<float(*)[2][HD]>(smem + Cfg::PARTS);
   __shared__ int pre[ATTN_THREADS], s_len[ATTN_THREADS];
   __shared__ int scratch[ATTN_WARPS + 1];
   __shared__ int s_before[ATTN_WARPS], s_pair[ATTN_WARPS];
-  __shared__ TileInfo s_info[ATTN_WARPS][ATTN_STAGES];
+  __shared__ TileInfo s_info[ATTN_WARPS][ATTN_INFOS];
   __shared__ int s_issued[ATTN_WARPS];   // tiles whose TileInfo is written
   __shared__ __align__(8) uint64_t full_bar[ATTN_WARPS][ATTN_STAGES], free_bar[ATTN_WARPS][ATTN_STAGES];
   __shared__ int s_abort;
@@ -281,79 +297,102 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
       i = (int)(r - (uint32_t)h * tiles);
       pages();
     }
-    int p_new = 0, owner = -1;
+    int p_new = 0, owner = -1, told = 0;
     int64_t t_new = 0;
+    // tells the consumer of the walk's tile
+    auto tell = [&]() {
+      if (owner != b) {
+        owner = b;
+        const int64_t p = a.next_pos ? a.next_pos[b] : n;
+        if (p < 0 || p > 0x7fffffff) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
+        p_new = p < 0 ? 0 : (p > 0x7fffffff ? 0x7fffffff : (int)p);
+        t_new = a.now ? a.now[b] : 0;
+      }
+      TileInfo info;
+      info.pair = b * H + h;
+      info.b = b;
+      info.h = h;
+      info.first = i * TILE;
+      info.left = n - i * TILE;
+      info.flags = i == 0;
+      info.p_new = p_new;
+      info.t_new = t_new;
+      info.to = info.to_slot = -1;
+#pragma unroll
+      for (int p = 0; p < NP; p++) {
+        const int left = info.left - PIECE * p, at = (i * TILE + PIECE * p) & (ps - 1);
+        if ((uint32_t)pg[p] >= (uint32_t)a.c.num_pages) {
+          if (left + a.append > 0) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
+          info.flags |= 2 << p;
+        }
+        info.slot[p] = ((int64_t)pg[p] << shift) + at;
+        info.row[p] = (((int64_t)pg[p] * H + h) << shift) + at;
+        if (a.append && left >= 0 && left < PIECE && !(code & 1) && !(info.flags & (2 << p))) {
+          info.to = info.row[p] + left;
+          if (h == 0) info.to_slot = info.slot[p] + left;
+        }
+      }
+      s_info[lane][told % ATTN_INFOS] = info;
+      __threadfence_block();
+      *reinterpret_cast<volatile int*>(&s_issued[lane]) = ++told;
+      if (told < count) {
+        if (++i == tiles) {
+          i = 0;
+          if (++h == H) {
+            h = 0;
+            code = -1;
+            while (code < 0 && b + 1 < B) code = length(++b);
+            n = code >> 1;
+            tiles = tiles_of(n);
+          }
+        }
+        pages();
+      }
+    };
+    // copies the cached rows of tile k; its barrier completes once it is also arrived on
+    auto fill = [&](int k) {
+      const int stage = k % ATTN_STAGES;
+      const TileInfo& t = s_info[lane][k % ATTN_INFOS];
+      uint64_t* bar = &full_bar[lane][stage];
+      unsigned char* dst = smem + (lane * ATTN_STAGES + stage) * STAGE;
+      int rows[NP], sum = 0;
+#pragma unroll
+      for (int p = 0; p < NP; p++) {
+        const int left = t.left - PIECE * p;
+        rows[p] = left <= 0 || (t.flags & (2 << p)) ? 0 : (left < PIECE ? left : PIECE);
+        sum += rows[p];
+      }
+      sm100::mbar_expect_tx(bar, (uint32_t)sum * 2 * ROW);
+      if (NP > 1 && ps >= TILE) {   // one page
+        rows[0] = sum;
+        rows[NP - 1] = 0;
+      }
+#pragma unroll
+      for (int p = 0; p < NP; p++) {
+        if (rows[p] == 0) continue;
+        const int64_t at = t.row[p] * HD;
+        bulk_load(dst + p * PIECE * ROW, static_cast<const T*>(a.c.k) + at, rows[p] * ROW, bar);
+        bulk_load(dst + ATTN_HALF + p * PIECE * ROW, static_cast<const T*>(a.c.v) + at, rows[p] * ROW, bar);
+      }
+    };
+    // A consumer that has seen tile k's barrier complete has been told of tiles k + 1 and k + 2: the
+    // arrival comes after.
+    if (count > 0) tell();
+    if (count > 0) fill(0);
+    if (count > 1) tell();
+    if (count > 1) fill(1);
+    for (; done < 2 && done < count; done++) {
+      if (told < count) tell();
+      sm100::mbar_arrive(&full_bar[lane][done]);
+    }
     uint64_t idle = 0;
     while (__any_sync(0xffffffffu, done < count)) {
       const int stage = done % ATTN_STAGES;
-      const bool go = done < count && (done < ATTN_STAGES ||
-                                       mbar_test(&free_bar[lane][stage], (done / ATTN_STAGES + 1) & 1));
-      if (go) {
-        if (owner != b) {
-          owner = b;
-          const int64_t p = a.next_pos ? a.next_pos[b] : n;
-          if (p < 0 || p > 0x7fffffff) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
-          p_new = p < 0 ? 0 : (p > 0x7fffffff ? 0x7fffffff : (int)p);
-          t_new = a.now ? a.now[b] : 0;
-        }
-        uint64_t* bar = &full_bar[lane][stage];
-        unsigned char* dst = smem + (lane * ATTN_STAGES + stage) * STAGE;
-        TileInfo info;
-        info.pair = b * H + h;
-        info.b = b;
-        info.h = h;
-        info.first = i * TILE;
-        info.left = n - i * TILE;
-        info.flags = i == 0;
-        info.p_new = p_new;
-        info.t_new = t_new;
-        info.to = info.to_slot = -1;
-        int rows[NP], sum = 0;
-#pragma unroll
-        for (int p = 0; p < NP; p++) {
-          const int left = info.left - PIECE * p, at = (i * TILE + PIECE * p) & (ps - 1);
-          rows[p] = left <= 0 ? 0 : (left < PIECE ? left : PIECE);
-          if ((uint32_t)pg[p] >= (uint32_t)a.c.num_pages) {
-            if (left + a.append > 0) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
-            info.flags |= 2 << p;
-            rows[p] = 0;
-          }
-          info.slot[p] = ((int64_t)pg[p] << shift) + at;
-          info.row[p] = (((int64_t)pg[p] * H + h) << shift) + at;
-          sum += rows[p];
-          if (a.append && left >= 0 && left < PIECE && !(code & 1) && !(info.flags & (2 << p))) {
-            info.to = info.row[p] + left;
-            if (h == 0) info.to_slot = info.slot[p] + left;
-          }
-        }
-        s_info[lane][stage] = info;
-        __threadfence_block();
-        *reinterpret_cast<volatile int*>(&s_issued[lane]) = done + 1;
-        sm100::mbar_arrive_expect_tx(bar, (uint32_t)sum * 2 * ROW);
-        if (NP > 1 && ps >= TILE) {   // one page
-          rows[0] = sum;
-          rows[NP - 1] = 0;
-        }
-#pragma unroll
-        for (int p = 0; p < NP; p++) {
-          if (rows[p] == 0) continue;
-          const int64_t at = info.row[p] * HD;
-          bulk_load(dst + p * PIECE * ROW, static_cast<const T*>(a.c.k) + at, rows[p] * ROW, bar);
-          bulk_load(dst + ATTN_HALF + p * PIECE * ROW, static_cast<const T*>(a.c.v) + at, rows[p] * ROW, bar);
-        }
-        if (++done < count) {
-          if (++i == tiles) {
-            i = 0;
-            if (++h == H) {
-              h = 0;
-              code = -1;
-              while (code < 0 && b + 1 < B) code = length(++b);
-              n = code >> 1;
-              tiles = tiles_of(n);
-            }
-          }
-          pages();
-        }
+      if (done < count && mbar_test(&free_bar[lane][stage], (done / ATTN_STAGES + 1) & 1)) {
+        fill(done);
+        if (told < count) tell();
+        sm100::mbar_arrive(&full_bar[lane][stage]);
+        done++;
         idle = 0;
       } else if (done < count) {
         // nothing to refill yet: bounded, as every wait of this kernel
@@ -372,51 +411,53 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
     const int count = (int)(share + ((uint32_t)gw < over ? 1 : 0));
     const int sub = lane % LPR, grp = lane / LPR;
     const int mine = (sub % 8) * RPI + grp;   // the lane's own row after the exchange of partial sums
-    // What a tile needs besides K and V, loaded while the tile before is worked on: the lane's own
-    // row's position, time and weight, and with the first tile the lane's piece of Q.  (The new
-    // token's K and V are loaded with the last tile.)
-    struct Ahead {
+    // What a tile needs besides K and V: the lane's own row's position, time and weight are loaded
+    // two tiles ahead, the biases that they select one tile ahead, the lane's piece of Q with the
+    // tile before a (sequence, head)'s first, those of the new token's K and V with its last.
+    struct __align__(16) Ahead {
+      int64_t t;
       int p;
       float w;
-      int64_t t;
     };
-    uint4 q, k_own, v_own, q_next;
-    q = k_own = v_own = q_next = make_uint4(0, 0, 0, 0);
+    Ahead(*rows)[32] = reinterpret_cast<Ahead(*)[32]>(smem + Cfg::ROWS) + warp * 2;
+    uint4 q, k_own, v_own;
+    q = k_own = v_own = make_uint4(0, 0, 0, 0);
+    auto new_row = [&](const TileInfo& t, int block) {   // the lane's piece of the new token's U, V, Q or K
+      return *reinterpret_cast<const uint4*>(static_cast<const T*>(a.uvqk) +
+                                             (((int64_t)t.b * 4 + block) * H + t.h) * HD + sub * E);
+    };
+    auto told_of = [&](int k) -> const TileInfo& { return s_info[warp][k % ATTN_INFOS]; };
     auto on_page = [&](const TileInfo& t) {   // the lane's own row is cached
       return mine < t.left && !(t.flags & (NP > 1 && mine >= PIECE ? 4 : 2));
     };
     auto place = [&](const int64_t* at) { return (NP > 1 && mine >= PIECE ? at[1] - PIECE : at[0]) + mine; };
-    auto look_ahead = [&](const TileInfo& t, bool fresh) {
-      Ahead r{t.first + mine, 0.0f, 0};
+    auto look_ahead = [&](int k) {   // each lane waits for and reads its own copies only
+      const TileInfo& t = told_of(k);
       if (on_page(t)) {
+        Ahead* r = &rows[k % 2][lane];
         const int64_t slot = place(t.slot);
-        if (a.c.positions && (a.pos || a.alibi)) r.p = a.c.positions[slot];
-        if (a.tim) r.t = a.c.timestamps[slot];
-        if (a.c.weights) r.w = a.c.weights[place(t.row)];
-      } else {   // the new token's own row is at distance 0
-        r.p = t.p_new;
-        r.t = t.t_new;
+        if (a.tim) copy_async<8>(&r->t, a.c.timestamps + slot);
+        if (a.c.positions && (a.pos || a.alibi)) copy_async<4>(&r->p, a.c.positions + slot);
+        if (a.c.weights) copy_async<4>(&r->w, a.c.weights + place(t.row));
       }
-      const T* u = static_cast<const T*>(a.uvqk) + ((int64_t)t.b * 4 * H + t.h) * HD + sub * E;
-      if (fresh) q_next = *reinterpret_cast<const uint4*>(u + 2LL * H * HD);
-      return r;
     };
-    auto bias_of = [&](const TileInfo& t, const Ahead& r) {
-      float x = 0.0f;
-      const int far = t.p_new - r.p, dist = far < 0 ? 0 : far;
-      if (a.pos) x = a.pos[(int64_t)t.h * a.P + (dist < a.P ? dist : a.P - 1)];
-      else if (a.alibi) x = -a.alibi[t.h] * (float)dist;
-      if (a.tim) x += a.tim[(int64_t)t.h * a.Tb + time_bucket(t.t_new - r.t, a.Tb)];
-      return x;
-    };
-    auto issued = [&](int k) {
-      const bool is = *reinterpret_cast<volatile int*>(&s_issued[warp]) > k;
-      __threadfence_block();
-      return __all_sync(0xffffffffu, is);
+    // loads tile k's biases (used one tile later) and its row's weight
+    float bias_p = 0.0f, bias_t = 0.0f, weight = 0.0f;
+    auto look_up = [&](int k) {
+      const TileInfo& t = told_of(k);
+      const bool cached = on_page(t);   // the new token's own row is at distance 0
+      const Ahead& r = rows[k % 2][lane];
+      if (a.pos || a.alibi) {
+        const int far = t.p_new - (a.c.positions ? r.p : t.first + mine), dist = cached && far > 0 ? far : 0;
+        if (a.pos) bias_p = a.pos[(int64_t)t.h * a.P + (dist < a.P ? dist : a.P - 1)];
+        else bias_p = -a.alibi[t.h] * (float)dist;
+      }
+      if (a.tim) bias_t = a.tim[(int64_t)t.h * a.Tb + time_bucket(cached ? t.t_new - r.t : 0, a.Tb)];
+      if (a.c.weights) weight = r.w;
     };
     auto await = [&](int k) {   // bounded, as every wait of this kernel
       const uint64_t t0 = sm100::globaltimer();
-      while (!issued(k)) {
+      while (!__all_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_issued[warp]) > k)) {
         if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort))) return false;
         if (__any_sync(0xffffffffu, sm100::globaltimer() - t0 > sm100::kWaitLimitNs)) {
           if (lane == 0) {
@@ -426,38 +467,40 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
           return false;
         }
       }
+      __threadfence_block();
       return true;
     };
     uint64_t acc[E / 2];
 #pragma unroll
     for (int e = 0; e < E / 2; e++) acc[e] = 0;
     bool whole = true, ok = true;   // whole: acc holds the (sequence, head) from its first tile on
-    float bias = 0.0f, weight = 0.0f;
     if (count > 0 && (ok = await(0))) {
-      const TileInfo& t = s_info[warp][0];
-      whole = t.flags & 1;
-      const Ahead r = look_ahead(t, true);
-      q = q_next;
-      bias = bias_of(t, r);
-      weight = r.w;
+      whole = told_of(0).flags & 1;
+      q = new_row(told_of(0), 2);
+      look_ahead(0);
+      copy_async_commit();
+      if (count > 1 && (ok = await(1))) look_ahead(1);
+      copy_async_commit();
+      copy_async_wait<1>();
+      look_up(0);
     }
     for (; ok && done < count; done++) {
       const int stage = done % ATTN_STAGES;
-      const TileInfo &info = s_info[warp][stage], &next = s_info[warp][(done + 1) % ATTN_STAGES];
+      const TileInfo &info = told_of(done), &next = told_of(done + 1);
       unsigned char* src = smem + (warp * ATTN_STAGES + stage) * STAGE;
       const int left = info.left, flags = info.flags, pair = info.pair;
-      const bool more = done + 1 < count, early = more && issued(done + 1);
-      const bool last = left < TILE;
-      Ahead ahead;
-      if (early) ahead = look_ahead(next, next.flags & 1);
+      const bool more = done + 1 < count, last = left < TILE;
+      uint4 q_next = q;
+      if (more && (next.flags & 1)) q_next = new_row(next, 2);
       if (last) {
-        const T* u = static_cast<const T*>(a.uvqk) + ((int64_t)info.b * 4 * H + info.h) * HD + sub * E;
-        k_own = *reinterpret_cast<const uint4*>(u + 3LL * H * HD);
-        v_own = *reinterpret_cast<const uint4*>(u + (int64_t)H * HD);
+        k_own = new_row(info, 3);
+        v_own = new_row(info, 1);
       }
       ok = sm100::mbar_wait(&full_bar[warp][stage], (done / ATTN_STAGES) & 1, &s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      if (done + 2 < count) look_ahead(done + 2);
+      copy_async_commit();
       const uint4* ks = reinterpret_cast<const uint4*>(src) + lane;
       const uint4* vs = ks + ATTN_HALF / 16;
       if (last) {
@@ -497,13 +540,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
       for (int w = 8; w < LPR; w <<= 1) part[0] += __shfl_xor_sync(0xffffffffu, part[0], w);
       float wgt = 0.0f;
       if (cached || mine == left) {
-        wgt = a.scale * silu_accurate(part[0] + bias);
+        wgt = a.scale * silu_accurate(part[0] + (bias_p + bias_t));
         if (a.c.weights && cached && sub < 8) a.c.weights[place(info.row)] = weight + fabsf(wgt);
       }
-      if (early) {
-        bias = bias_of(next, ahead);
-        weight = ahead.w;
-      }
+      copy_async_wait<1>();   // tile done + 1's rows
+      if (more) look_up(done + 1);
       const bool full = left >= TILE && !(flags & ~1);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
@@ -559,14 +600,6 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
 #pragma unroll
         for (int e = 0; e < E / 2; e++) acc[e] = 0;
         whole = true;
-      }
-      if (more && !early) {
-        ok = await(done + 1);
-        if (ok) {
-          const Ahead r = look_ahead(next, next.flags & 1);
-          bias = bias_of(next, r);
-          weight = r.w;
-        }
       }
       q = q_next;
     }
