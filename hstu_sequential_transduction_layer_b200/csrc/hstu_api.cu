@@ -364,8 +364,10 @@ hstu_status_t check_cache(const hstu_paged_cache_t* c) {
   return HSTU_OK;
 }
 
+int row_bytes(const hstu_paged_cache_t& c) { return c.head_dim * (c.dtype == HSTU_BF16 ? 2 : 4); }
+
 size_t cache_bytes(const hstu_paged_cache_t& c) {   // of K, and of V
-  return (size_t)c.num_pages * c.page_size * c.num_heads * c.head_dim * (c.dtype == HSTU_BF16 ? 2 : 4);
+  return (size_t)c.num_pages * c.page_size * c.num_heads * row_bytes(c);
 }
 
 // Does [p, p + n) overlap any array of the cache?
@@ -1074,16 +1076,12 @@ hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seq
   if (total_tokens == 0) return HSTU_OK;
   if (num_seqs == 0 || !uvqk || !seq_offsets || !aligned16(uvqk)) return HSTU_ERR_INVALID_ARG;
   if (cache->timestamps && !timestamps) return HSTU_ERR_INVALID_ARG;
-  const size_t row = (size_t)4 * cache->num_heads * cache->head_dim * (cache->dtype == HSTU_BF16 ? 2 : 4);
-  if (overlaps_cache(uvqk, (size_t)total_tokens * row, *cache)) return HSTU_ERR_INVALID_ARG;
-  if (total_tokens * cache->num_heads / 8 >= (1LL << 31) - 1) return HSTU_ERR_UNSUPPORTED;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  check_offsets_kernel<<<(unsigned)((num_seqs + 1 + 255) / 256), 256, 0, st>>>(seq_offsets, num_seqs,
-                                                                              total_tokens);
-  if (launch_status() != HSTU_OK) return HSTU_ERR_CUDA;
-  return paged::launch_append(cache_view(*cache), cache->dtype, cache->head_dim, total_tokens,
-                              num_seqs, uvqk, seq_offsets, timestamps, page_table, max_pages,
-                              cache_lens, next_positions, st);
+  if (overlaps_cache(uvqk, (size_t)total_tokens * 4 * cache->num_heads * row_bytes(*cache), *cache))
+    return HSTU_ERR_INVALID_ARG;
+  if (total_tokens / paged::APPEND_TOKENS >= (1LL << 31) - 1) return HSTU_ERR_UNSUPPORTED;
+  return paged::launch_append(cache_view(*cache), row_bytes(*cache), total_tokens, num_seqs, uvqk,
+                              seq_offsets, timestamps, page_table, max_pages, cache_lens,
+                              next_positions, static_cast<cudaStream_t>(stream));
 }
 
 size_t hstu_paged_attention_workspace_size(const hstu_shape_t* shape) {
@@ -1176,7 +1174,7 @@ hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs
   if (!cache->positions || !cache->weights) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_table(cache->page_size, num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
   if (num_seqs == 0) return HSTU_OK;
-  if (num_seqs > 65535) return HSTU_ERR_UNSUPPORTED;
+  if (num_seqs >= (1LL << 27)) return HSTU_ERR_UNSUPPORTED;
   if (!new_lens || !workspace) return HSTU_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) return HSTU_ERR_INVALID_ARG;
   const int64_t room = max_pages * cache->page_size;
@@ -1203,7 +1201,7 @@ hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs
   a.count = w.count;
   a.room = room;
   a.moves = w.moves;
-  return paged::launch_evict(a, cache->dtype, cache->head_dim, static_cast<cudaStream_t>(stream));
+  return paged::launch_evict(a, row_bytes(*cache), tc::num_sms(), static_cast<cudaStream_t>(stream));
 }
 
 size_t hstu_stochastic_length_workspace_size(int64_t num_seqs) {

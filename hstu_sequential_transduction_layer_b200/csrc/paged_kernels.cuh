@@ -9,6 +9,8 @@
 // i % page_size.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "sm100.cuh"
 
@@ -539,6 +541,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
 #pragma unroll
       for (int w = 8; w < LPR; w <<= 1) part[0] += __shfl_xor_sync(0xffffffffu, part[0], w);
       float wgt = 0.0f;
+      // only here: added where they are loaded, the two would be waited for a tile early
+      asm volatile("" : "+f"(bias_p), "+f"(bias_t));
       if (cached || mine == left) {
         wgt = a.scale * silu_accurate(part[0] + (bias_p + bias_t));
         if (a.c.weights && cached && sub < 8) a.c.weights[place(info.row)] = weight + fabsf(wgt);
@@ -697,50 +701,78 @@ __global__ void __launch_bounds__(ATTN_MAX_CTAS) attention_join_kernel(float* av
 }
 
 // Rows of a jagged U|V|Q|K batch into the cache: token t of sequence b goes to slot lens[b] + (t -
-// off[b]).  One warp per (token, head).
-template <typename T>
-__global__ void __launch_bounds__(256) append_kernel(const Cache c, int HD, int64_t Tn, int64_t B,
-                                                     const T* __restrict__ uvqk,
+// off[b]).  A CTA takes APPEND_TOKENS tokens: a thread a token finds its sequence by bisection and its
+// row's place, then all threads copy, 16 bytes at a time; K and V rows are read in order, 1 to 8 KB a
+// token, and written as the heads' separate rows of 128 bytes or more.  HBM-bound.
+constexpr int APPEND_TOKENS = 16;
+template <int LPR>
+__global__ void __launch_bounds__(256) append_kernel(const Cache c, int64_t Tn, int64_t B,
+                                                     const uint4* __restrict__ uvqk,
                                                      const int64_t* __restrict__ off,
                                                      const int64_t* __restrict__ ts,
                                                      const int32_t* __restrict__ table,
                                                      int64_t max_pages,
                                                      const int64_t* __restrict__ lens,
                                                      const int64_t* __restrict__ next_pos) {
-  constexpr int E = vec16<T>::N;
-  const int lane = threadIdx.x % 32;
-  const int64_t item = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-  if (item >= Tn * c.H) return;
-  const int64_t t = item / c.H;
-  const int h = (int)(item % c.H);
-  // the last sequence that starts at or before t and has not ended by then
-  int64_t lo = 0, hi = B;   // off[lo] <= t < off[hi]
-  if (t < off[0] || t >= off[B]) return;   // reported by the offsets check
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (off[mid] <= t) lo = mid; else hi = mid;
+  __shared__ int64_t s_row[APPEND_TOKENS];   // the token's row of head 0, or -1
+  // the offsets' own check, over all CTAs
+  for (int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x; s <= B; s += (int64_t)gridDim.x * 256) {
+    const int64_t v = off[s];
+    if ((s == 0 && v != 0) || (s == B && v != Tn) || v < 0 || v > Tn || (s > 0 && off[s - 1] > v))
+      report(HSTU_ERR_DEVICE_BAD_OFFSETS);
   }
-  const int64_t i = t - off[lo], n = lens[lo], slot = n + i, room = max_pages << c.ps_shift;
-  if (n < 0 || i < 0 || n >= room || slot >= room) {
-    if (lane == 0) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
-    return;
+  const int64_t t0 = (int64_t)blockIdx.x * APPEND_TOKENS;
+  const int shift = c.ps_shift, ps = 1 << shift, H = c.H;
+  if (threadIdx.x < APPEND_TOKENS) {
+    const int64_t t = t0 + threadIdx.x;
+    int64_t row = -1;
+    if (t < Tn && t >= off[0] && t < off[B]) {
+      int64_t lo = 0, hi = B;   // off[lo] <= t < off[hi]
+      while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) / 2;
+        if (off[mid] <= t) lo = mid; else hi = mid;
+      }
+      const int64_t i = t - off[lo], n = lens[lo], slot = n + i, room = max_pages << shift;
+      if (n < 0 || n >= room || slot >= room) {
+        report(HSTU_ERR_DEVICE_BAD_OFFSETS);
+      } else {
+        const int64_t pg = page_of(table + lo * max_pages, slot >> shift, c.num_pages);
+        if (pg >= 0) {
+          const int64_t o = slot & (ps - 1), at = (pg << shift) + o;
+          row = ((pg * H) << shift) + o;
+          if (c.positions) c.positions[at] = (int32_t)((next_pos ? next_pos[lo] : n) + i);
+          if (c.timestamps && ts) c.timestamps[at] = ts[t];
+        }
+      }
+    }
+    s_row[threadIdx.x] = row;
   }
-  const int64_t pg = page_of(table + lo * max_pages, slot >> c.ps_shift, c.num_pages);
-  if (pg < 0) return;
-  const int ps = 1 << c.ps_shift, o = (int)(slot & (ps - 1));
-  const int64_t to = (((pg * c.H + h) << c.ps_shift) + o) * HD;
-  const T* src = uvqk + t * 4 * c.H * HD + (int64_t)h * HD;
-  for (int e = lane * E; e < HD; e += 32 * E) {
-    *reinterpret_cast<uint4*>(static_cast<T*>(c.k) + to + e) =
-        *reinterpret_cast<const uint4*>(src + 3LL * c.H * HD + e);
-    *reinterpret_cast<uint4*>(static_cast<T*>(c.v) + to + e) =
-        *reinterpret_cast<const uint4*>(src + (int64_t)c.H * HD + e);
-  }
-  if (lane == 0) {
-    if (c.weights) c.weights[((pg * c.H + h) << c.ps_shift) + o] = 0.0f;
-    if (h == 0) {
-      if (c.positions) c.positions[(pg << c.ps_shift) + o] = (int32_t)((next_pos ? next_pos[lo] : n) + i);
-      if (c.timestamps && ts) c.timestamps[(pg << c.ps_shift) + o] = ts[t];
+  __syncthreads();
+  // piece x of a token: 16 bytes of K and of V; head x / LPR
+  const int width = H * LPR, total = APPEND_TOKENS * width;
+  constexpr int U = 4;
+  for (int x0 = threadIdx.x; x0 < total; x0 += 256 * U) {
+    uint4 k[U], v[U];
+    int64_t to[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int x = x0 + u * 256, t = x / width, e = x - t * width;
+      to[u] = -1;
+      if (x < total && s_row[t] >= 0) {
+        const int h = e / LPR;
+        to[u] = s_row[t] + ((int64_t)h << shift);
+        const uint4* src = uvqk + (t0 + t) * 4 * width + e;
+        v[u] = __ldcs(src + width);
+        k[u] = __ldcs(src + 3 * width);
+        if (e % LPR == 0 && c.weights) c.weights[to[u]] = 0.0f;
+        to[u] = to[u] * LPR + e % LPR;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (to[u] < 0) continue;
+      static_cast<uint4*>(c.k)[to[u]] = k[u];
+      static_cast<uint4*>(c.v)[to[u]] = v[u];
     }
   }
 }
@@ -777,152 +809,271 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One thread per slot of every sequence that has to lose tokens.
-__global__ void __launch_bounds__(256) evict_keys_kernel(const Evict a) {
-  const int64_t b = blockIdx.y;
-  const int64_t n = cached_len(a.lens[b], a.room);
-  if (n <= a.budget) return;
-  const int ps = 1 << a.c.ps_shift;
-  for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < n; j += (int64_t)gridDim.x * 256) {
-    const int64_t pg = page_of(a.table + b * a.max_pages, j >> a.c.ps_shift, a.c.num_pages);
-    uint32_t key = 0;
-    if (pg >= 0) {
-      const int64_t o = j & (ps - 1);
-      double s = 0.0;
-      for (int h = 0; h < a.c.H; h++) s += (double)a.c.weights[((pg * a.c.H + h) << a.c.ps_shift) + o];
-      key = weight_key((float)s);
-      const int64_t next = a.next_pos ? a.next_pos[b] : n;
-      if ((int64_t)a.c.positions[(pg << a.c.ps_shift) + o] >= next - a.recent) key = KEY_RECENT;
-    }
-    a.keys[b * a.room + j] = key;
-  }
-}
+// Selection, one cluster of CTAs per sequence, each on a contiguous part of its slots.  Every thread
+// scores its slots (the first SEL_KEYS keys stay in registers, any further ones go through the
+// workspace), the budget-th largest key is found 4 bits at a time from the top, and the gaps below
+// slot `budget` and the kept slots from there on are listed in ascending order.  A pass over the keys
+// counts digits without atomics, whatever the weights' distribution: a thread's SEL_KEYS digits in
+// 16 4-bit fields, sums over the warp, the CTA and (through distributed shared memory) the cluster.
+// Bound by latency: some 10 dependent steps, each of a few hundred clocks.
+constexpr int SEL_THREADS = 1024, SEL_KEYS = 8, SEL_CLUSTER = 8;
 
-constexpr int SEL_THREADS = 1024;
-
-// Exclusive prefix sums of two counts per thread, packed in one int64 (each below 2^31).
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  int64_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) scratch[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t w = scratch[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    scratch[lane] = w;
-  }
-  __syncthreads();
-  const int64_t before = (warp > 0 ? scratch[warp - 1] : 0) + x - v;
-  __syncthreads();
-  return before;
-}
-
-// One CTA per sequence: the budget-th largest key by radix select, 8 bits a pass, then the gaps
-// below slot `budget` and the kept slots above it, both in ascending order.
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a) {
-  __shared__ unsigned int hist[256];
-  __shared__ int64_t scratch[32];
-  __shared__ uint32_t s_digit;
-  __shared__ int64_t s_k;
-  const int tid = threadIdx.x;
-  const int64_t b = blockIdx.x;
-  const int64_t len = a.lens[b], n = cached_len(len, a.room);
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  __shared__ int s_warp[32][16];               // digits of a warp; later, counts before each warp
+  __shared__ int s_all[2][SEL_CLUSTER][16];    // digits of each CTA of the cluster
+  __shared__ int64_t s_count[SEL_CLUSTER][2];  // counts of each CTA of the cluster
+  __shared__ int64_t s_scan[32];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t b = blockIdx.x / S, len = a.lens[b], n = cached_len(len, a.room);
   if (n <= a.budget) {
-    if (tid == 0) {
+    if (rank == 0 && tid == 0) {
       a.new_lens[b] = len < 0 ? len : n;
       a.count[b] = 0;
     }
     return;
   }
-  const uint32_t* keys = a.keys + b * a.room;
+  const int shift = a.c.ps_shift, ps = 1 << shift, H = a.c.H;
+  const int32_t* pages = a.table + b * a.max_pages;
+  const int64_t per = ((n + S - 1) / S + 31) / 32 * 32;
+  const int64_t lo = rank * per < n ? rank * per : n, hi = lo + per < n ? lo + per : n;
+  const int64_t rounds = (hi - lo + SEL_THREADS - 1) / SEL_THREADS;
+  const int64_t oldest = (a.next_pos ? a.next_pos[b] : n) - a.recent;
+  uint32_t* spill = a.keys + b * a.room + lo;
+  auto slot_of = [&](int64_t r) { return lo + r * SEL_THREADS + tid; };
+
+  uint32_t key[SEL_KEYS];
+#pragma unroll
+  for (int i = 0; i < SEL_KEYS; i++) key[i] = 0;
+#pragma unroll 1
+  for (int64_t r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
+#pragma unroll
+    for (int i = 0; i < SEL_KEYS; i++) {
+      const int64_t j = slot_of(r0 + i);
+      if (j >= hi) continue;
+      const int64_t pg = page_of(pages, j >> shift, a.c.num_pages);
+      uint32_t k = 0;
+      if (pg >= 0) {
+        const int o = (int)(j & (ps - 1));
+        const float* w = a.c.weights + ((pg * H) << shift) + o;
+        double s = 0.0;
+#pragma unroll 8
+        for (int h = 0; h < H; h++) s += (double)w[(int64_t)h << shift];
+        k = weight_key((float)s);
+        if ((int64_t)a.c.positions[(pg << shift) + o] >= oldest) k = KEY_RECENT;
+      }
+      if (r0 == 0) key[i] = k; else spill[(r0 + i) * SEL_THREADS + tid] = k;
+    }
+  }
+  // keys of rounds r0 .. r0 + SEL_KEYS - 1
+  auto keys_at = [&](int64_t r0, uint32_t (&k)[SEL_KEYS]) {
+#pragma unroll
+    for (int i = 0; i < SEL_KEYS; i++)
+      k[i] = r0 == 0 ? key[i] : (slot_of(r0 + i) < hi ? spill[(r0 + i) * SEL_THREADS + tid] : 0u);
+  };
+
   uint32_t prefix = 0, mask = 0;
-  int64_t k = a.budget;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int d = tid; d < 256; d += SEL_THREADS) hist[d] = 0;
-    __syncthreads();
-    for (int64_t j = tid; j < n; j += SEL_THREADS) {
-      const uint32_t key = keys[j];
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+  int64_t want = a.budget;    // of the keys that share the prefix, how many are kept
+  bool ties = true;           // fewer of them are kept than there are
+  int buf = 0;
+#pragma unroll 1
+  for (int sh = 28; sh >= 0; sh -= 4, buf ^= 1) {
+    int mine = 0;             // lane l < 16: the warp's keys with digit l
+#pragma unroll 1
+    for (int64_t r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
+      uint32_t k[SEL_KEYS];
+      keys_at(r0, k);
+      uint64_t digits = 0;
+#pragma unroll
+      for (int i = 0; i < SEL_KEYS; i++)
+        if (slot_of(r0 + i) < hi && (k[i] & mask) == prefix) digits += 1ull << (4 * ((k[i] >> sh) & 15));
+#pragma unroll
+      for (int f = 0; f < 8; f++) {
+        const uint32_t two = (uint32_t)(digits >> (8 * f)) & 255u;
+        const uint32_t sum = __reduce_add_sync(0xffffffffu, (two & 15u) | (two >> 4) << 16);
+        if (lane >> 1 == f) mine += lane & 1 ? sum >> 16 : sum & 0xffffu;
+      }
     }
+    if (lane < 16) s_warp[warp][lane] = mine;
     __syncthreads();
-    if (tid == 0) {
-      int64_t cum = 0;
-      int d = 255;
-      while (d > 0 && cum + hist[d] < k) cum += hist[d--];
-      s_digit = d;
-      s_k = k - cum;
+    if (warp < 16) {
+      const int sum = __reduce_add_sync(0xffffffffu, s_warp[lane][warp]);
+      if (lane < S) *cluster.map_shared_rank(&s_all[buf][rank][warp], lane) = sum;
     }
+    if (S > 1) cluster.sync(); else __syncthreads();
+    int64_t total = 0;
+    if (lane < 16)
+      for (int r = 0; r < S; r++) total += s_all[buf][r][lane];
+    // the highest digit at which the running count from the top reaches `want`
+    int64_t from_top = total;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      const int64_t y = __shfl_down_sync(0xffffffffu, from_top, o);
+      if (lane + o < 16) from_top += y;
+    }
+    const unsigned reach = __ballot_sync(0xffffffffu, lane < 16 && from_top >= want);
+    const int d = reach ? 31 - __clz(reach) : 0;
+    const int64_t in_d = __shfl_sync(0xffffffffu, total, d);
+    want -= __shfl_sync(0xffffffffu, from_top, d) - in_d;
+    prefix |= (uint32_t)d << sh;
+    mask |= 15u << sh;
+    if (in_d == want) {       // all of them are kept: every key >= prefix
+      ties = false;
+      break;
+    }
+  }
+
+  // Sums over the slots before a thread's, in slot order, of two flags a slot: a round's flags by
+  // ballot, the warps' counts by a scan, the CTAs' by their exchange.
+  auto flags_of = [&](int64_t r0, const uint32_t (&k)[SEL_KEYS], int64_t& seen, uint32_t (&gap)[SEL_KEYS],
+                      uint32_t (&mover)[SEL_KEYS]) {
+    // per round, the warp's ballots of gaps and kept slots past the budget; `seen` counts the equal
+    // keys before the CTA's rounds so far
+#pragma unroll
+    for (int i = 0; i < SEL_KEYS; i++) {
+      const int64_t j = slot_of(r0 + i);
+      const bool in = j < hi, same = in && k[i] == prefix;
+      bool keep = in && (ties ? k[i] > prefix : k[i] >= prefix);
+      if (ties) {
+        const unsigned m = __ballot_sync(0xffffffffu, same);
+        __syncthreads();
+        if (lane == 0) s_warp[warp][0] = __popc(m);
+        __syncthreads();
+        const int cnt = s_warp[lane][0];
+        const int below = __reduce_add_sync(0xffffffffu, lane < warp ? cnt : 0);
+        const int64_t before = seen + below + __popc(m & ((1u << lane) - 1u));
+        seen += __reduce_add_sync(0xffffffffu, cnt);
+        keep = keep || (same && before < want);
+      }
+      gap[i] = __ballot_sync(0xffffffffu, in && j < a.budget && !keep);
+      mover[i] = __ballot_sync(0xffffffffu, in && j >= a.budget && keep);
+    }
+  };
+  // each CTA's count of a quantity, told to the cluster; returns the sum over the CTAs before this one
+  auto before_cta = [&](int64_t mine, int which) {
+    if (tid < S) *cluster.map_shared_rank(&s_count[rank][which], tid) = mine;
+    if (S > 1) cluster.sync(); else __syncthreads();
+    int64_t sum = 0;
+    for (int r = 0; r < rank; r++) sum += s_count[r][which];
+    return sum;
+  };
+  int64_t eq_before = 0;
+  if (ties) {
+    int64_t eq = 0;
+#pragma unroll 1
+    for (int64_t r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
+      uint32_t k[SEL_KEYS];
+      keys_at(r0, k);
+#pragma unroll
+      for (int i = 0; i < SEL_KEYS; i++) eq += slot_of(r0 + i) < hi && k[i] == prefix ? 1 : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    if (lane == 0) s_scan[warp] = eq;
     __syncthreads();
-    prefix |= s_digit << shift;
-    mask |= 255u << shift;
-    k = s_k;
-    __syncthreads();
+    eq = 0;
+    for (int w = 0; w < 32; w++) eq += s_scan[w];
+    eq_before = before_cta(eq, 0);
   }
-  // kept: key > prefix, and the first k slots whose key equals it
-  const int64_t per = (n + SEL_THREADS - 1) / SEL_THREADS;
-  const int64_t j0 = tid * per < n ? tid * per : n, j1 = j0 + per < n ? j0 + per : n;
-  int64_t eq = 0;
-  for (int64_t j = j0; j < j1; j++) eq += keys[j] == prefix ? 1 : 0;
-  const int64_t eq0 = block_scan(eq, scratch);
-  int64_t both = 0, seen = eq0;
-  for (int64_t j = j0; j < j1; j++) {
-    const bool same = keys[j] == prefix, keep = keys[j] > prefix || (same && seen < k);
-    seen += same ? 1 : 0;
-    if (j < a.budget && !keep) both += 1;
-    if (j >= a.budget && keep) both += 1LL << 32;
+  // gaps and movers: counted first, so that the CTAs know where theirs begin (a sequence has as many
+  // of either; low half gaps, high half movers)
+  int64_t base = 0;
+#pragma unroll 1
+  for (int pass = S > 1 ? 0 : 1; pass < 2; pass++) {
+    int64_t seen = eq_before, run = base;
+#pragma unroll 1
+    for (int64_t r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
+      uint32_t k[SEL_KEYS], gap[SEL_KEYS], mover[SEL_KEYS];
+      keys_at(r0, k);
+      flags_of(r0, k, seen, gap, mover);
+      __syncthreads();
+      // s_warp[w][i]: warp w's gaps (low half) and movers (high half) of round i
+      if (lane < SEL_KEYS) {
+        uint32_t g = 0, m = 0;
+#pragma unroll
+        for (int i = 0; i < SEL_KEYS; i++)
+          if (lane == i) {
+            g = gap[i];
+            m = mover[i];
+          }
+        s_warp[warp][lane] = __popc(g) | __popc(m) << 16;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < SEL_KEYS; i++) {
+        const uint32_t cnt = (uint32_t)s_warp[lane][i];   // halves of at most 32 * 32: no carry
+        const uint32_t below = __reduce_add_sync(0xffffffffu, lane < warp ? cnt : 0u);
+        const uint32_t all = __reduce_add_sync(0xffffffffu, cnt);
+        if (pass) {
+          const uint32_t bit = 1u << lane;
+          const bool is_gap = gap[i] & bit, is_mover = mover[i] & bit;
+          if (is_gap || is_mover) {
+            const int64_t j = slot_of(r0 + i);
+            const int64_t pg = page_of(pages, j >> shift, a.c.num_pages);
+            const int64_t flat = pg < 0 ? -1 : (pg << shift) + (j & (ps - 1));
+            const int64_t at = (is_gap ? (run & 0xffffffffLL) + (below & 0xffffu) : (run >> 32) + (below >> 16)) +
+                               __popc((is_gap ? gap[i] : mover[i]) & (bit - 1u));
+            (is_gap ? a.to : a.from)[b * a.moves + at] = flat;
+          }
+        }
+        run += (int64_t)(all & 0xffffu) + ((int64_t)(all >> 16) << 32);
+      }
+    }
+    if (pass == 0) {
+      base = before_cta(run, 1);
+    } else if (hi == n && lo < n && tid == 0) {   // the last CTA with slots has seen them all
+      a.count[b] = run & 0xffffffffLL;
+      a.new_lens[b] = a.budget;
+    }
   }
-  const int64_t before = block_scan(both, scratch);
-  int64_t gaps = before & 0xffffffffLL, movers = before >> 32;
-  seen = eq0;
-  const int ps = 1 << a.c.ps_shift;
-  for (int64_t j = j0; j < j1; j++) {
-    const bool same = keys[j] == prefix, keep = keys[j] > prefix || (same && seen < k);
-    seen += same ? 1 : 0;
-    if ((j < a.budget) == keep) continue;
-    const int64_t pg = page_of(a.table + b * a.max_pages, j >> a.c.ps_shift, a.c.num_pages);
-    const int64_t flat = pg < 0 ? -1 : (pg << a.c.ps_shift) + (j & (ps - 1));
-    if (keep) a.from[b * a.moves + movers++] = flat; else a.to[b * a.moves + gaps++] = flat;
-  }
-  if (tid == SEL_THREADS - 1) {
-    a.count[b] = gaps;   // as many gaps below the budget as kept slots above it
-    a.new_lens[b] = a.budget;
-  }
+  if (S > 1) cluster.sync();   // no CTA leaves while another may write to its shared memory
 }
 
 // Moves the kept rows into the gaps.  Sources lie at or above slot `budget`, destinations below it,
-// so rows move in any order.  One warp per (move, head).
-template <typename T>
-__global__ void __launch_bounds__(256) evict_move_kernel(const Evict a, int HD) {
-  constexpr int E = vec16<T>::N;
-  const int64_t b = blockIdx.y, count = a.count[b];
-  const int lane = threadIdx.x % 32, ps = 1 << a.c.ps_shift, H = a.c.H;
-  for (int64_t it = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; it < count * H;
-       it += (int64_t)gridDim.x * 8) {
-    const int64_t m = it / H;
-    const int h = (int)(it % H);
-    const int64_t to = a.to[b * a.moves + m], from = a.from[b * a.moves + m];
-    if (to < 0 || from < 0) continue;
-    const int64_t rt = ((((to >> a.c.ps_shift) * H + h) << a.c.ps_shift) + (to & (ps - 1)));
-    const int64_t rf = ((((from >> a.c.ps_shift) * H + h) << a.c.ps_shift) + (from & (ps - 1)));
-    for (int e = lane * E; e < HD; e += 32 * E) {
-      T *k = static_cast<T*>(a.c.k), *v = static_cast<T*>(a.c.v);
-      *reinterpret_cast<uint4*>(k + rt * HD + e) = *reinterpret_cast<const uint4*>(k + rf * HD + e);
-      *reinterpret_cast<uint4*>(v + rt * HD + e) = *reinterpret_cast<const uint4*>(v + rf * HD + e);
+// so rows move in any order.  LPR lanes of 16 bytes a (token, head), K and V; HBM-bound.
+template <int LPR>
+__global__ void __launch_bounds__(256) evict_move_kernel(const Evict a, int ctas) {
+  constexpr int R = 256 / LPR, U = 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t b = blockIdx.x / ctas;
+  const int part = (int)(blockIdx.x % ctas);
+  const int H = a.c.H, shift = a.c.ps_shift, ps = 1 << shift, sub = threadIdx.x % LPR;
+  const int64_t items = a.count[b] * H;
+  const int64_t *tos = a.to + b * a.moves, *froms = a.from + b * a.moves;
+  uint4 *k = static_cast<uint4*>(a.c.k), *v = static_cast<uint4*>(a.c.v);
+  for (int64_t x0 = (int64_t)part * R * U + threadIdx.x / LPR; x0 < items; x0 += (int64_t)ctas * R * U) {
+    uint4 kr[U], vr[U];
+    int64_t rt[U], rf[U], to[U], from[U];
+    int h[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t x = x0 + u * R;
+      rt[u] = -1;
+      if (x >= items) continue;
+      const int64_t m = x / H;
+      h[u] = (int)(x - m * H);
+      to[u] = tos[m];
+      from[u] = froms[m];
+      if (to[u] < 0 || from[u] < 0) continue;
+      rt[u] = ((((to[u] >> shift) * H + h[u]) << shift) + (to[u] & (ps - 1)));
+      rf[u] = ((((from[u] >> shift) * H + h[u]) << shift) + (from[u] & (ps - 1)));
+      kr[u] = k[rf[u] * LPR + sub];
+      vr[u] = v[rf[u] * LPR + sub];
     }
-    if (lane == 0) {
-      a.c.weights[rt] = a.c.weights[rf];
-      if (h == 0) {
-        a.c.positions[to] = a.c.positions[from];
-        if (a.c.timestamps) a.c.timestamps[to] = a.c.timestamps[from];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (rt[u] < 0) continue;
+      k[rt[u] * LPR + sub] = kr[u];
+      v[rt[u] * LPR + sub] = vr[u];
+      if (sub == 0) {
+        a.c.weights[rt[u]] = a.c.weights[rf[u]];
+        if (h[u] == 0) {
+          a.c.positions[to[u]] = a.c.positions[from[u]];
+          if (a.c.timestamps) a.c.timestamps[to[u]] = a.c.timestamps[from[u]];
+        }
       }
     }
   }
@@ -989,30 +1140,43 @@ inline hstu_status_t launch_attention(const Attn& a, int dtype, int hd, void* ws
                     : launch_attention_t<float, 128>(a, ws, sms, st);
 }
 
-inline hstu_status_t launch_append(const Cache& c, int dtype, int hd, int64_t T, int64_t B,
+inline hstu_status_t launch_append(const Cache& c, int row_bytes, int64_t T, int64_t B,
                                    const void* uvqk, const int64_t* off, const int64_t* ts,
                                    const int32_t* table, int64_t max_pages, const int64_t* lens,
                                    const int64_t* next_pos, cudaStream_t st) {
-  const unsigned grid = (unsigned)((T * c.H + 7) / 8);
-  if (dtype == HSTU_BF16)
-    append_kernel<bf16><<<grid, 256, 0, st>>>(c, hd, T, B, (const bf16*)uvqk, off, ts, table,
-                                              max_pages, lens, next_pos);
-  else
-    append_kernel<float><<<grid, 256, 0, st>>>(c, hd, T, B, (const float*)uvqk, off, ts, table,
-                                               max_pages, lens, next_pos);
+  const unsigned grid = (unsigned)((T + APPEND_TOKENS - 1) / APPEND_TOKENS);
+  auto kern = row_bytes == 128 ? append_kernel<8> : row_bytes == 256 ? append_kernel<16> : append_kernel<32>;
+  kern<<<grid, 256, 0, st>>>(c, T, B, static_cast<const uint4*>(uvqk), off, ts, table, max_pages, lens,
+                             next_pos);
   return launched();
 }
 
-inline hstu_status_t launch_evict(const Evict& a, int dtype, int hd, cudaStream_t st) {
-  hstu_status_t rc;
-  const unsigned gx = (unsigned)(a.room < 256 * 64 ? (a.room + 255) / 256 : 64);
-  evict_keys_kernel<<<dim3(gx, (unsigned)a.B), 256, 0, st>>>(a);
-  if ((rc = launched()) != HSTU_OK) return rc;
-  evict_select_kernel<<<(unsigned)a.B, SEL_THREADS, 0, st>>>(a);
-  if ((rc = launched()) != HSTU_OK) return rc;
-  const dim3 grid(64, (unsigned)a.B);
-  if (dtype == HSTU_BF16) evict_move_kernel<bf16><<<grid, 256, 0, st>>>(a, hd);
-  else evict_move_kernel<float><<<grid, 256, 0, st>>>(a, hd);
+inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaStream_t st) {
+  cudaLaunchAttribute attr[1]{};
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // one CTA for each 4096 slots a row may have, at most 8
+  int S = 1;
+  while (S < SEL_CLUSTER && (int64_t)S * 4096 < a.room) S *= 2;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(a.B * S));
+  cfg.blockDim = dim3(SEL_THREADS);
+  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess) return HSTU_ERR_CUDA;
+  hstu_status_t rc = launched();
+  if (rc != HSTU_OK) return rc;
+  // eight CTAs a SM over all sequences, at least one each
+  int64_t ctas = (8LL * sms + a.B - 1) / a.B;
+  attr[0] = cudaLaunchAttribute{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its launch overlaps the selection
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(a.B * ctas));
+  cfg.blockDim = dim3(256);
+  auto kern = row_bytes == 128 ? evict_move_kernel<8> : row_bytes == 256 ? evict_move_kernel<16> : evict_move_kernel<32>;
+  if (cudaLaunchKernelEx(&cfg, kern, a, (int)ctas) != cudaSuccess) return HSTU_ERR_CUDA;
   return launched();
 }
 
