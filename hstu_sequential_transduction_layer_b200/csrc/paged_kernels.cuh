@@ -809,227 +809,258 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Selection, one cluster of CTAs per sequence, each on a contiguous part of its slots.  Every thread
-// scores its slots (the first SEL_KEYS keys stay in registers, any further ones go through the
-// workspace), the budget-th largest key is found 4 bits at a time from the top, and the gaps below
-// slot `budget` and the kept slots from there on are listed in ascending order.  A pass over the keys
-// counts digits without atomics, whatever the weights' distribution: a thread's SEL_KEYS digits in
-// 16 4-bit fields, sums over the warp, the CTA and (through distributed shared memory) the cluster.
-// Bound by latency: some 10 dependent steps, each of a few hundred clocks.
-constexpr int SEL_THREADS = 1024, SEL_KEYS = 8, SEL_CLUSTER = 8;
+// Selection, one cluster of CTAs per sequence, each on a contiguous part of its slots, each warp on a
+// contiguous part of that.  Every thread scores its slots: the first SEL_KEYS keys stay in registers,
+// and all of a sequence's keys are gathered in the first CTA's shared memory (in the workspace, where
+// a row's slots do not fit).  That CTA finds the budget-th largest key by histograms of the top 12,
+// the next 10 and the last 10 bits; then every CTA lists the gaps below slot `budget` and the kept
+// slots from there on among its own, in ascending order.  Twelve bits (three of the mantissa) spread
+// accumulated weights over enough bins that the shared-memory atomics seldom meet; warps whose keys
+// all fall into one bin add them at once.  Bound by latency: some ten dependent steps.
+constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32, SEL_KEYS = 8, SEL_CLUSTER = 8;
+constexpr int SEL_SMEM_KEYS = 49152;
 
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  __shared__ int s_warp[32][16];               // digits of a warp; later, counts before each warp
-  __shared__ int s_all[2][SEL_CLUSTER][16];    // digits of each CTA of the cluster
-  __shared__ int64_t s_count[SEL_CLUSTER][2];  // counts of each CTA of the cluster
-  __shared__ int64_t s_scan[32];
+  __shared__ __align__(16) int s_hist[4096 + 1024 + 1024];
+  __shared__ int s_warp[SEL_WARPS], s_gaps[SEL_WARPS], s_movers[SEL_WARPS];
+  __shared__ int s_count[3][SEL_CLUSTER];      // equal keys, gaps and movers of the cluster's CTAs
+  __shared__ int s_bin, s_want, s_in;
+  __shared__ uint32_t s_found[3];              // the search's prefix, want and ties
+  extern __shared__ uint32_t s_keys[];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t b = blockIdx.x / S, len = a.lens[b], n = cached_len(len, a.room);
-  if (n <= a.budget) {
+  const int64_t b = blockIdx.x / S, len = a.lens[b], n64 = cached_len(len, a.room);
+  if (n64 <= a.budget) {
     if (rank == 0 && tid == 0) {
-      a.new_lens[b] = len < 0 ? len : n;
+      a.new_lens[b] = len < 0 ? len : n64;
       a.count[b] = 0;
     }
     return;
   }
+  auto sync = [&]() {
+    if (S > 1) cluster.sync(); else __syncthreads();
+  };
+  const int n = (int)n64, budget = (int)a.budget;   // slots are numbered in 31 bits
   const int shift = a.c.ps_shift, ps = 1 << shift, H = a.c.H;
   const int32_t* pages = a.table + b * a.max_pages;
-  const int64_t per = ((n + S - 1) / S + 31) / 32 * 32;
-  const int64_t lo = rank * per < n ? rank * per : n, hi = lo + per < n ? lo + per : n;
-  const int64_t rounds = (hi - lo + SEL_THREADS - 1) / SEL_THREADS;
-  const int64_t oldest = (a.next_pos ? a.next_pos[b] : n) - a.recent;
-  uint32_t* spill = a.keys + b * a.room + lo;
-  auto slot_of = [&](int64_t r) { return lo + r * SEL_THREADS + tid; };
+  // the warp's slots: `rounds` times 32
+  const int rounds = (n + S * SEL_THREADS - 1) / (S * SEL_THREADS);
+  const int start = (rank * SEL_WARPS + warp) * rounds * 32 + lane;   // < n + 32 * S * SEL_THREADS
+  const int64_t oldest = (a.next_pos ? a.next_pos[b] : n64) - a.recent;
+  uint32_t* spill = a.keys + b * a.room;
+  uint32_t* all_keys = a.room <= SEL_SMEM_KEYS ? cluster.map_shared_rank(s_keys, 0) : spill;
 
+  if (rank == 0)
+    for (int i = tid; i < (4096 + 1024 + 1024) / 4; i += SEL_THREADS)
+      reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
+
+  // scores: the loads of all slots and two heads are in flight at once
   uint32_t key[SEL_KEYS];
-#pragma unroll
-  for (int i = 0; i < SEL_KEYS; i++) key[i] = 0;
 #pragma unroll 1
-  for (int64_t r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
+  for (int r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
+    int64_t at[SEL_KEYS];
+    int pos[SEL_KEYS];
+    double sum[SEL_KEYS];
+    unsigned live = 0;
 #pragma unroll
     for (int i = 0; i < SEL_KEYS; i++) {
-      const int64_t j = slot_of(r0 + i);
-      if (j >= hi) continue;
-      const int64_t pg = page_of(pages, j >> shift, a.c.num_pages);
-      uint32_t k = 0;
-      if (pg >= 0) {
-        const int o = (int)(j & (ps - 1));
-        const float* w = a.c.weights + ((pg * H) << shift) + o;
-        double s = 0.0;
-#pragma unroll 8
-        for (int h = 0; h < H; h++) s += (double)w[(int64_t)h << shift];
-        k = weight_key((float)s);
-        if ((int64_t)a.c.positions[(pg << shift) + o] >= oldest) k = KEY_RECENT;
-      }
-      if (r0 == 0) key[i] = k; else spill[(r0 + i) * SEL_THREADS + tid] = k;
+      const int j = start + (r0 + i) * 32;
+      at[i] = r0 + i < rounds && j < n ? pages[j >> shift] : 0;
+      sum[i] = 0.0;
     }
-  }
-  // keys of rounds r0 .. r0 + SEL_KEYS - 1
-  auto keys_at = [&](int64_t r0, uint32_t (&k)[SEL_KEYS]) {
-#pragma unroll
-    for (int i = 0; i < SEL_KEYS; i++)
-      k[i] = r0 == 0 ? key[i] : (slot_of(r0 + i) < hi ? spill[(r0 + i) * SEL_THREADS + tid] : 0u);
-  };
-
-  uint32_t prefix = 0, mask = 0;
-  int64_t want = a.budget;    // of the keys that share the prefix, how many are kept
-  bool ties = true;           // fewer of them are kept than there are
-  int buf = 0;
-#pragma unroll 1
-  for (int sh = 28; sh >= 0; sh -= 4, buf ^= 1) {
-    int mine = 0;             // lane l < 16: the warp's keys with digit l
-#pragma unroll 1
-    for (int64_t r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
-      uint32_t k[SEL_KEYS];
-      keys_at(r0, k);
-      uint64_t digits = 0;
-#pragma unroll
-      for (int i = 0; i < SEL_KEYS; i++)
-        if (slot_of(r0 + i) < hi && (k[i] & mask) == prefix) digits += 1ull << (4 * ((k[i] >> sh) & 15));
-#pragma unroll
-      for (int f = 0; f < 8; f++) {
-        const uint32_t two = (uint32_t)(digits >> (8 * f)) & 255u;
-        const uint32_t sum = __reduce_add_sync(0xffffffffu, (two & 15u) | (two >> 4) << 16);
-        if (lane >> 1 == f) mine += lane & 1 ? sum >> 16 : sum & 0xffffu;
-      }
-    }
-    if (lane < 16) s_warp[warp][lane] = mine;
-    __syncthreads();
-    if (warp < 16) {
-      const int sum = __reduce_add_sync(0xffffffffu, s_warp[lane][warp]);
-      if (lane < S) *cluster.map_shared_rank(&s_all[buf][rank][warp], lane) = sum;
-    }
-    if (S > 1) cluster.sync(); else __syncthreads();
-    int64_t total = 0;
-    if (lane < 16)
-      for (int r = 0; r < S; r++) total += s_all[buf][r][lane];
-    // the highest digit at which the running count from the top reaches `want`
-    int64_t from_top = total;
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-      const int64_t y = __shfl_down_sync(0xffffffffu, from_top, o);
-      if (lane + o < 16) from_top += y;
-    }
-    const unsigned reach = __ballot_sync(0xffffffffu, lane < 16 && from_top >= want);
-    const int d = reach ? 31 - __clz(reach) : 0;
-    const int64_t in_d = __shfl_sync(0xffffffffu, total, d);
-    want -= __shfl_sync(0xffffffffu, from_top, d) - in_d;
-    prefix |= (uint32_t)d << sh;
-    mask |= 15u << sh;
-    if (in_d == want) {       // all of them are kept: every key >= prefix
-      ties = false;
-      break;
-    }
-  }
-
-  // Sums over the slots before a thread's, in slot order, of two flags a slot: a round's flags by
-  // ballot, the warps' counts by a scan, the CTAs' by their exchange.
-  auto flags_of = [&](int64_t r0, const uint32_t (&k)[SEL_KEYS], int64_t& seen, uint32_t (&gap)[SEL_KEYS],
-                      uint32_t (&mover)[SEL_KEYS]) {
-    // per round, the warp's ballots of gaps and kept slots past the budget; `seen` counts the equal
-    // keys before the CTA's rounds so far
 #pragma unroll
     for (int i = 0; i < SEL_KEYS; i++) {
-      const int64_t j = slot_of(r0 + i);
-      const bool in = j < hi, same = in && k[i] == prefix;
-      bool keep = in && (ties ? k[i] > prefix : k[i] >= prefix);
-      if (ties) {
-        const unsigned m = __ballot_sync(0xffffffffu, same);
-        __syncthreads();
-        if (lane == 0) s_warp[warp][0] = __popc(m);
-        __syncthreads();
-        const int cnt = s_warp[lane][0];
-        const int below = __reduce_add_sync(0xffffffffu, lane < warp ? cnt : 0);
-        const int64_t before = seen + below + __popc(m & ((1u << lane) - 1u));
-        seen += __reduce_add_sync(0xffffffffu, cnt);
-        keep = keep || (same && before < want);
+      const int j = start + (r0 + i) * 32;
+      if (r0 + i < rounds && j < n) {
+        if (at[i] >= 0 && at[i] < a.c.num_pages) live |= 1u << i;
+        else report(HSTU_ERR_DEVICE_BAD_OFFSETS);
       }
-      gap[i] = __ballot_sync(0xffffffffu, in && j < a.budget && !keep);
-      mover[i] = __ballot_sync(0xffffffffu, in && j >= a.budget && keep);
+      if (!(live >> i & 1)) at[i] = 0;   // any slot: the value is dropped
+      const int o = j & (ps - 1);
+      pos[i] = a.c.positions[(at[i] << shift) + o];
+      at[i] = ((at[i] * H) << shift) + o;
     }
-  };
-  // each CTA's count of a quantity, told to the cluster; returns the sum over the CTAs before this one
-  auto before_cta = [&](int64_t mine, int which) {
-    if (tid < S) *cluster.map_shared_rank(&s_count[rank][which], tid) = mine;
-    if (S > 1) cluster.sync(); else __syncthreads();
-    int64_t sum = 0;
-    for (int r = 0; r < rank; r++) sum += s_count[r][which];
-    return sum;
-  };
-  int64_t eq_before = 0;
-  if (ties) {
-    int64_t eq = 0;
 #pragma unroll 1
-    for (int64_t r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
-      uint32_t k[SEL_KEYS];
-      keys_at(r0, k);
+    for (int h = 0; h < H; h += 2) {
+      float w[2][SEL_KEYS];
 #pragma unroll
-      for (int i = 0; i < SEL_KEYS; i++) eq += slot_of(r0 + i) < hi && k[i] == prefix ? 1 : 0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) eq += __shfl_xor_sync(0xffffffffu, eq, o);
-    if (lane == 0) s_scan[warp] = eq;
-    __syncthreads();
-    eq = 0;
-    for (int w = 0; w < 32; w++) eq += s_scan[w];
-    eq_before = before_cta(eq, 0);
-  }
-  // gaps and movers: counted first, so that the CTAs know where theirs begin (a sequence has as many
-  // of either; low half gaps, high half movers)
-  int64_t base = 0;
-#pragma unroll 1
-  for (int pass = S > 1 ? 0 : 1; pass < 2; pass++) {
-    int64_t seen = eq_before, run = base;
-#pragma unroll 1
-    for (int64_t r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
-      uint32_t k[SEL_KEYS], gap[SEL_KEYS], mover[SEL_KEYS];
-      keys_at(r0, k);
-      flags_of(r0, k, seen, gap, mover);
-      __syncthreads();
-      // s_warp[w][i]: warp w's gaps (low half) and movers (high half) of round i
-      if (lane < SEL_KEYS) {
-        uint32_t g = 0, m = 0;
+      for (int u = 0; u < 2; u++)
 #pragma unroll
         for (int i = 0; i < SEL_KEYS; i++)
-          if (lane == i) {
-            g = gap[i];
-            m = mover[i];
-          }
-        s_warp[warp][lane] = __popc(g) | __popc(m) << 16;
-      }
-      __syncthreads();
+          w[u][i] = i < rounds && h + u < H ? a.c.weights[at[i] + ((int64_t)(h + u) << shift)] : 0.0f;
 #pragma unroll
-      for (int i = 0; i < SEL_KEYS; i++) {
-        const uint32_t cnt = (uint32_t)s_warp[lane][i];   // halves of at most 32 * 32: no carry
-        const uint32_t below = __reduce_add_sync(0xffffffffu, lane < warp ? cnt : 0u);
-        const uint32_t all = __reduce_add_sync(0xffffffffu, cnt);
-        if (pass) {
-          const uint32_t bit = 1u << lane;
-          const bool is_gap = gap[i] & bit, is_mover = mover[i] & bit;
-          if (is_gap || is_mover) {
-            const int64_t j = slot_of(r0 + i);
-            const int64_t pg = page_of(pages, j >> shift, a.c.num_pages);
-            const int64_t flat = pg < 0 ? -1 : (pg << shift) + (j & (ps - 1));
-            const int64_t at = (is_gap ? (run & 0xffffffffLL) + (below & 0xffffu) : (run >> 32) + (below >> 16)) +
-                               __popc((is_gap ? gap[i] : mover[i]) & (bit - 1u));
-            (is_gap ? a.to : a.from)[b * a.moves + at] = flat;
-          }
-        }
-        run += (int64_t)(all & 0xffffu) + ((int64_t)(all >> 16) << 32);
-      }
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < SEL_KEYS; i++) sum[i] += (double)w[u][i];
     }
-    if (pass == 0) {
-      base = before_cta(run, 1);
-    } else if (hi == n && lo < n && tid == 0) {   // the last CTA with slots has seen them all
-      a.count[b] = run & 0xffffffffLL;
-      a.new_lens[b] = a.budget;
+#pragma unroll
+    for (int i = 0; i < SEL_KEYS; i++) {
+      const int j = start + (r0 + i) * 32;
+      uint32_t k = (int64_t)pos[i] >= oldest ? KEY_RECENT : weight_key((float)sum[i]);
+      if (!(live >> i & 1)) k = 0;
+      if (r0 == 0) key[i] = k;
+      if (r0 + i < rounds && j < n) all_keys[j] = k;
     }
   }
-  if (S > 1) cluster.sync();   // no CTA leaves while another may write to its shared memory
+  // f(slot, key, whether there is such a slot) for the warp's slots in order; all lanes take part
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < SEL_KEYS; i++)
+      if (i < rounds) f(start + i * 32, key[i], start + i * 32 < n);
+#pragma unroll 1
+    for (int r = SEL_KEYS; r < rounds; r++) {
+      const int j = start + r * 32;
+      f(j, j < n ? spill[j] : 0u, j < n);
+    }
+  };
+  sync();
+
+  uint32_t prefix = 0, mask = 0;
+  int want = budget;          // of the keys that share the prefix, how many are kept
+  bool ties = true;           // fewer of them are kept than there are
+  if (rank == 0) {
+  int* hist = s_hist;
+  const uint32_t* keys = a.room <= SEL_SMEM_KEYS ? s_keys : spill;
+#pragma unroll 1
+  for (int sh = 20, bits = 12; sh >= 0; sh -= 10, bits = 10) {
+    const uint32_t low = (1u << bits) - 1u;
+#pragma unroll 4
+    for (int j0 = warp * 32; j0 < n; j0 += SEL_THREADS) {
+      const int j = j0 + lane;
+      const uint32_t k = j < n ? keys[j] : 0u;
+      const bool counts = j < n && (k & mask) == prefix;
+      const int bin = counts ? (int)(k >> sh & low) : -1;
+      int one;
+      __match_all_sync(0xffffffffu, bin, &one);
+      if (one) {
+        if (lane == 0 && counts) atomicAdd(&hist[bin], 32);
+      } else if (counts) {
+        atomicAdd(&hist[bin], 1);
+      }
+    }
+    __syncthreads();
+    // thread t: bins t * W .. t * W + W - 1
+    const int W = (int)(low + 1) / SEL_THREADS;   // 4 or 1
+    int own = 0, c[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      c[i] = i < W ? hist[tid * W + i] : 0;
+      own += c[i];
+    }
+    int top = own;   // keys in the thread's bins and those of the lanes above
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_down_sync(0xffffffffu, top, o);
+      if (lane + o < 32) top += y;
+    }
+    if (lane == 0) s_warp[warp] = top;
+    __syncthreads();
+    top += __reduce_add_sync(0xffffffffu, lane > warp && lane < SEL_WARPS ? s_warp[lane] : 0);
+    if (want == 0 ? tid == SEL_THREADS - 1 : top >= want && top - own < want) {
+      int above = top - own, d = W - 1;
+#pragma unroll
+      for (int i = 3; i > 0; i--)
+        if (i < W && d == i && above + c[i] < want) {
+          above += c[i];
+          d = i - 1;
+        }
+      s_bin = tid * W + d;
+      s_want = want - above;
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (i == d) s_in = c[i];
+    }
+    __syncthreads();
+    prefix |= (uint32_t)s_bin << sh;
+    mask |= low << sh;
+    want = s_want;
+    ties = s_in != want;
+    hist += low + 1;
+    if (!ties) break;         // all of them are kept: every key >= prefix
+    __syncthreads();          // before the next round's s_bin
+  }
+    if (tid < 3 * S)
+      cluster.map_shared_rank(s_found, tid / 3)[tid % 3] = tid % 3 == 0 ? prefix : tid % 3 == 1 ? (uint32_t)want : ties;
+  }
+  sync();
+  prefix = s_found[0];
+  want = (int)s_found[1];
+  ties = s_found[2];
+
+  // the CTAs' counts of one quantity, told to the cluster; the sum over the CTAs before this one
+  auto before_cta = [&](int which) {
+    int sum = 0;
+    for (int r = 0; r < rank; r++) sum += s_count[which][r];
+    return sum;
+  };
+  auto tell = [&](int which, int mine) {
+    if (tid < S) *cluster.map_shared_rank(&s_count[which][rank], tid) = mine;
+  };
+  int equal = 0;              // with ties: equal keys in slots before the warp's
+  if (ties) {
+    int cnt = 0;
+    each([&](int, uint32_t k, bool in) { cnt += __popc(__ballot_sync(0xffffffffu, in && k == prefix)); });
+    if (lane == 0) s_warp[warp] = cnt;
+    __syncthreads();
+    const int w = lane < SEL_WARPS ? s_warp[lane] : 0;
+    equal = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    tell(0, __reduce_add_sync(0xffffffffu, w));
+    sync();
+    equal += before_cta(0);
+  }
+  // f(slot, lanes whose slot is a gap, lanes whose slot moves) for the warp's slots in order
+  auto each_flagged = [&](auto f) {
+    int seen = equal;
+    each([&](int j, uint32_t k, bool in) {
+      bool keep = in && k >= prefix;
+      if (ties) {
+        const unsigned same = __ballot_sync(0xffffffffu, in && k == prefix);
+        keep = in && (k > prefix || (k == prefix && seen + __popc(same & ((1u << lane) - 1u)) < want));
+        seen += __popc(same);
+      }
+      f(j, __ballot_sync(0xffffffffu, in && j < budget && !keep),
+        __ballot_sync(0xffffffffu, in && j >= budget && keep));
+    });
+  };
+  int gaps = 0, movers = 0;
+  each_flagged([&](int, unsigned g, unsigned m) {
+    gaps += __popc(g);
+    movers += __popc(m);
+  });
+  if (lane == 0) {
+    s_gaps[warp] = gaps;
+    s_movers[warp] = movers;
+  }
+  __syncthreads();
+  const int wg = lane < SEL_WARPS ? s_gaps[lane] : 0, wm = lane < SEL_WARPS ? s_movers[lane] : 0;
+  int gap_at = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0);
+  int mover_at = __reduce_add_sync(0xffffffffu, lane < warp ? wm : 0);
+  tell(1, __reduce_add_sync(0xffffffffu, wg));
+  tell(2, __reduce_add_sync(0xffffffffu, wm));
+  sync();
+  gap_at += before_cta(1);
+  mover_at += before_cta(2);
+  if (rank == 0 && tid == 0) {
+    int all = 0;
+    for (int r = 0; r < S; r++) all += s_count[1][r];
+    a.count[b] = all;         // as many gaps below the budget as kept slots from there on
+    a.new_lens[b] = budget;
+  }
+  each_flagged([&](int j, unsigned g, unsigned m) {
+    const unsigned bit = 1u << lane;
+    if ((g | m) & bit) {
+      const int64_t pg = page_of(pages, j >> shift, a.c.num_pages);
+      const int64_t flat = pg < 0 ? -1 : (pg << shift) + (j & (ps - 1));
+      if (g & bit) a.to[b * a.moves + gap_at + __popc(g & (bit - 1u))] = flat;
+      else a.from[b * a.moves + mover_at + __popc(m & (bit - 1u))] = flat;
+    }
+    gap_at += __popc(g);
+    mover_at += __popc(m);
+  });
+  if (S > 1) cluster.sync();   // no CTA leaves while another may read or write its shared memory
 }
 
 // Moves the kept rows into the gaps.  Sources lie at or above slot `budget`, destinations below it,
@@ -1157,20 +1188,26 @@ inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaSt
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // one CTA for each 4096 slots a row may have, at most 8
+  // as many CTAs as hold the keys of a row's slots in registers, at most 8
   int S = 1;
-  while (S < SEL_CLUSTER && (int64_t)S * 4096 < a.room) S *= 2;
+  while (S < SEL_CLUSTER && (int64_t)S * SEL_THREADS * SEL_KEYS < a.room) S *= 2;
+  const int smem = a.room <= SEL_SMEM_KEYS ? (int)a.room * 4 : 0;
+  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           SEL_SMEM_KEYS * 4) != cudaSuccess)
+    return HSTU_ERR_CUDA;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = S;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(a.B * S));
   cfg.blockDim = dim3(SEL_THREADS);
+  cfg.dynamicSmemBytes = smem;
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess) return HSTU_ERR_CUDA;
   hstu_status_t rc = launched();
   if (rc != HSTU_OK) return rc;
   // eight CTAs a SM over all sequences, at least one each
   int64_t ctas = (8LL * sms + a.B - 1) / a.B;
   attr[0] = cudaLaunchAttribute{};
+  cfg.dynamicSmemBytes = 0;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its launch overlaps the selection
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)(a.B * ctas));
