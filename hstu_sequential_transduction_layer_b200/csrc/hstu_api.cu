@@ -358,6 +358,8 @@ hstu_status_t check_cache(const hstu_paged_cache_t* c) {
     return HSTU_ERR_INVALID_ARG;
   if (!paged::head_dim_supported(c->dtype, c->head_dim)) return HSTU_ERR_UNSUPPORTED;
   if (4LL * c->num_heads * c->head_dim > (1LL << 30)) return HSTU_ERR_INVALID_ARG;
+  // rows of K, V and weights are numbered in 32 bits (2^32 rows of K alone are 512 GB and more)
+  if (c->num_pages * c->page_size >= (1LL << 32) / c->num_heads) return HSTU_ERR_UNSUPPORTED;
   if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) || !aligned16(c->positions) ||
       !aligned16(c->timestamps) || !aligned16(c->weights))
     return HSTU_ERR_INVALID_ARG;

@@ -810,26 +810,29 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
 }
 
 // Selection, one cluster of CTAs per sequence, each on a contiguous part of its slots, each warp on a
-// contiguous part of that.  Every thread scores its slots: the first SEL_KEYS keys stay in registers,
-// and all of a sequence's keys are gathered in the first CTA's shared memory (in the workspace, where
-// a row's slots do not fit).  That CTA finds the budget-th largest key by histograms of the top 12,
-// the next 10 and the last 10 bits; then every CTA lists the gaps below slot `budget` and the kept
-// slots from there on among its own, in ascending order.  Twelve bits (three of the mantissa) spread
-// accumulated weights over enough bins that the shared-memory atomics seldom meet; warps whose keys
-// all fall into one bin add them at once.  Bound by latency: some ten dependent steps.
-constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32, SEL_KEYS = 8, SEL_CLUSTER = 8;
-constexpr int SEL_SMEM_KEYS = 49152;
+// contiguous part of that.  Every thread scores its slots; the first SEL_KEYS keys stay in registers,
+// any further ones go through the workspace.  The budget-th largest key is found by histograms of the
+// top 11, the next 11 and the last 10 bits: every CTA counts its own keys and adds its occupied bins
+// to the first CTA's, which finds the bin and tells the others; once few keys share the bits found
+// so far, the first CTA gets those keys and finishes alone.  Then every CTA lists the gaps below slot
+// `budget` and the kept slots from there on among its own, in ascending order.  Eleven bits (two of
+// the mantissa) spread accumulated weights over enough bins that the shared-memory atomics seldom
+// meet; warps whose keys all fall into one bin add them at once.  Bound by latency, some ten
+// dependent steps, and by the instructions of code that runs once: few warps, and several CTAs.
+constexpr int SEL_THREADS = 256, SEL_WARPS = SEL_THREADS / 32, SEL_KEYS = 8, SEL_CLUSTER = 8;
+constexpr int SEL_BINS = 2048, SEL_LIST = 1024;
 
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  __shared__ __align__(16) int s_hist[4096 + 1024 + 1024];
+  __shared__ __align__(16) int s_hist[3][SEL_BINS];
+  __shared__ uint32_t s_list[SEL_LIST];
+  __shared__ int s_listed;
   __shared__ int s_warp[SEL_WARPS], s_gaps[SEL_WARPS], s_movers[SEL_WARPS];
   __shared__ int s_count[3][SEL_CLUSTER];      // equal keys, gaps and movers of the cluster's CTAs
-  __shared__ int s_bin, s_want, s_in;
-  __shared__ uint32_t s_found[3];              // the search's prefix, want and ties
-  extern __shared__ uint32_t s_keys[];
+  __shared__ int s_found[3];                   // the bin that holds the key searched, how many of its
+                                               // keys are kept, and how many there are
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t b = blockIdx.x / S, len = a.lens[b], n64 = cached_len(len, a.room);
@@ -851,50 +854,49 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   const int start = (rank * SEL_WARPS + warp) * rounds * 32 + lane;   // < n + 32 * S * SEL_THREADS
   const int64_t oldest = (a.next_pos ? a.next_pos[b] : n64) - a.recent;
   uint32_t* spill = a.keys + b * a.room;
-  uint32_t* all_keys = a.room <= SEL_SMEM_KEYS ? cluster.map_shared_rank(s_keys, 0) : spill;
 
-  if (rank == 0)
-    for (int i = tid; i < (4096 + 1024 + 1024) / 4; i += SEL_THREADS)
-      reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
+  if (tid == 0) s_listed = 0;
+  for (int i = tid; i < 3 * SEL_BINS / 4; i += SEL_THREADS)
+    reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
 
-  // scores: the loads of all slots and two heads are in flight at once
+  // scores: the loads of SEL_KEYS slots and four heads are in flight at once
   uint32_t key[SEL_KEYS];
 #pragma unroll 1
   for (int r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
-    int64_t at[SEL_KEYS];
+    uint32_t at[SEL_KEYS];      // rows of weights: below 2^32
     int pos[SEL_KEYS];
     double sum[SEL_KEYS];
     unsigned live = 0;
 #pragma unroll
     for (int i = 0; i < SEL_KEYS; i++) {
       const int j = start + (r0 + i) * 32;
-      at[i] = r0 + i < rounds && j < n ? pages[j >> shift] : 0;
+      at[i] = r0 + i < rounds && j < n ? (uint32_t)pages[j >> shift] : 0u;
       sum[i] = 0.0;
     }
 #pragma unroll
     for (int i = 0; i < SEL_KEYS; i++) {
       const int j = start + (r0 + i) * 32;
       if (r0 + i < rounds && j < n) {
-        if (at[i] >= 0 && at[i] < a.c.num_pages) live |= 1u << i;
+        if (at[i] < (uint32_t)a.c.num_pages) live |= 1u << i;
         else report(HSTU_ERR_DEVICE_BAD_OFFSETS);
       }
       if (!(live >> i & 1)) at[i] = 0;   // any slot: the value is dropped
       const int o = j & (ps - 1);
-      pos[i] = a.c.positions[(at[i] << shift) + o];
-      at[i] = ((at[i] * H) << shift) + o;
+      pos[i] = a.c.positions[((int64_t)at[i] << shift) + o];
+      at[i] = ((at[i] * (uint32_t)H) << shift) + o;
     }
 #pragma unroll 1
-    for (int h = 0; h < H; h += 2) {
-      float w[2][SEL_KEYS];
+    for (int h = 0; h < H; h += 4) {
+      float w[4][SEL_KEYS];
 #pragma unroll
-      for (int u = 0; u < 2; u++)
+      for (int u = 0; u < 4; u++)
 #pragma unroll
         for (int i = 0; i < SEL_KEYS; i++)
-          w[u][i] = i < rounds && h + u < H ? a.c.weights[at[i] + ((int64_t)(h + u) << shift)] : 0.0f;
+          w[u][i] = __ldg(a.c.weights + at[i] + ((uint32_t)(h + u < H ? h + u : H - 1) << shift));
 #pragma unroll
-      for (int u = 0; u < 2; u++)
+      for (int u = 0; u < 4; u++)
 #pragma unroll
-        for (int i = 0; i < SEL_KEYS; i++) sum[i] += (double)w[u][i];
+        for (int i = 0; i < SEL_KEYS; i++) sum[i] += h + u < H ? (double)w[u][i] : 0.0;
     }
 #pragma unroll
     for (int i = 0; i < SEL_KEYS; i++) {
@@ -902,7 +904,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       uint32_t k = (int64_t)pos[i] >= oldest ? KEY_RECENT : weight_key((float)sum[i]);
       if (!(live >> i & 1)) k = 0;
       if (r0 == 0) key[i] = k;
-      if (r0 + i < rounds && j < n) all_keys[j] = k;
+      else if (r0 + i < rounds && j < n) spill[j] = k;
     }
   }
   // f(slot, key, whether there is such a slot) for the warp's slots in order; all lanes take part
@@ -916,41 +918,37 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       f(j, j < n ? spill[j] : 0u, j < n);
     }
   };
-  sync();
+  sync();   // bins are zero everywhere
 
   uint32_t prefix = 0, mask = 0;
   int want = budget;          // of the keys that share the prefix, how many are kept
-  bool ties = true;           // fewer of them are kept than there are
-  if (rank == 0) {
-  int* hist = s_hist;
-  const uint32_t* keys = a.room <= SEL_SMEM_KEYS ? s_keys : spill;
-#pragma unroll 1
-  for (int sh = 20, bits = 12; sh >= 0; sh -= 10, bits = 10) {
-    const uint32_t low = (1u << bits) - 1u;
-#pragma unroll 4
-    for (int j0 = warp * 32; j0 < n; j0 += SEL_THREADS) {
-      const int j = j0 + lane;
-      const uint32_t k = j < n ? keys[j] : 0u;
-      const bool counts = j < n && (k & mask) == prefix;
-      const int bin = counts ? (int)(k >> sh & low) : -1;
-      int one;
-      __match_all_sync(0xffffffffu, bin, &one);
-      if (one) {
-        if (lane == 0 && counts) atomicAdd(&hist[bin], 32);
-      } else if (counts) {
-        atomicAdd(&hist[bin], 1);
-      }
+  int in_bin = n;             // and how many there are
+  // counts a warp's keys into bins; all lanes take part
+  auto count = [&](int* hist, uint32_t k, bool counts, int sh, uint32_t low) {
+    const unsigned m = __ballot_sync(0xffffffffu, counts);
+    if (m == 0) return;
+    const int bin = (int)(k >> sh & low), lead = __ffs(m) - 1;
+    const int its = __shfl_sync(0xffffffffu, bin, lead);
+    if (__ballot_sync(0xffffffffu, counts && bin == its) == m) {
+      if (lane == lead) atomicAdd(&hist[bin], __popc(m));
+    } else if (counts) {
+      atomicAdd(&hist[bin], 1);
     }
-    __syncthreads();
-    // thread t: bins t * W .. t * W + W - 1
-    const int W = (int)(low + 1) / SEL_THREADS;   // 4 or 1
-    int own = 0, c[4];
+  };
+  // the highest bin at which the count from the top reaches `want`, for all CTAs of `tell_to`
+  auto find = [&](const int* hist, int tell_to) {
+    constexpr int PER = SEL_BINS / SEL_THREADS;
+    int c[PER], own = 0;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      c[i] = i < W ? hist[tid * W + i] : 0;
-      own += c[i];
+    for (int i = 0; i < PER; i += 4) {
+      const int4 x = *reinterpret_cast<const int4*>(hist + tid * PER + i);
+      c[i] = x.x;
+      c[i + 1] = x.y;
+      c[i + 2] = x.z;
+      c[i + 3] = x.w;
+      own += x.x + x.y + x.z + x.w;
     }
-    int top = own;   // keys in the thread's bins and those of the lanes above
+    int top = own;            // keys in the thread's bins and those above
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_down_sync(0xffffffffu, top, o);
@@ -960,35 +958,95 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
     __syncthreads();
     top += __reduce_add_sync(0xffffffffu, lane > warp && lane < SEL_WARPS ? s_warp[lane] : 0);
     if (want == 0 ? tid == SEL_THREADS - 1 : top >= want && top - own < want) {
-      int above = top - own, d = W - 1;
+      int above = top - own, d = PER - 1, at = c[PER - 1];
 #pragma unroll
-      for (int i = 3; i > 0; i--)
-        if (i < W && d == i && above + c[i] < want) {
+      for (int i = PER - 1; i > 0; i--)
+        if (d == i && above + c[i] < want) {
           above += c[i];
+          at = c[i - 1];
           d = i - 1;
         }
-      s_bin = tid * W + d;
-      s_want = want - above;
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (i == d) s_in = c[i];
+      for (int r = 0; r < tell_to; r++) {
+        int* to = cluster.map_shared_rank(s_found, r);
+        to[0] = tid * PER + d;
+        to[1] = want - above;
+        to[2] = at;
+      }
     }
-    __syncthreads();
-    prefix |= (uint32_t)s_bin << sh;
+  };
+  auto take = [&](int sh, uint32_t low) {
+    prefix |= (uint32_t)s_found[0] << sh;
     mask |= low << sh;
-    want = s_want;
-    ties = s_in != want;
-    hist += low + 1;
-    if (!ties) break;         // all of them are kept: every key >= prefix
-    __syncthreads();          // before the next round's s_bin
+    want = s_found[1];
+    in_bin = s_found[2];
+  };
+  int sh = 21, pass = 0;
+  bool listed = false;
+#pragma unroll 1
+  for (; pass < 3 && in_bin != want; pass++) {
+    const uint32_t low = pass < 2 ? 2047u : 1023u;
+    int* hist = s_hist[pass];
+    if (pass > 0 && in_bin <= SEL_LIST) {
+      listed = true;
+      break;
+    }
+    each([&](int, uint32_t k, bool in) { count(hist, k, in && (k & mask) == prefix, sh, low); });
+    __syncthreads();
+    if (S > 1) {
+      int* to = cluster.map_shared_rank(hist, 0);
+      if (rank > 0)
+        for (int i = tid; i < SEL_BINS; i += SEL_THREADS)
+          if (hist[i]) atomicAdd(to + i, hist[i]);
+      cluster.sync();
+    }
+    if (rank == 0) find(hist, S);
+    sync();
+    take(sh, low);
+    sh = pass == 0 ? 10 : 0;
+    if (S == 1) __syncthreads();   // s_found is read before it is written again
   }
-    if (tid < 3 * S)
-      cluster.map_shared_rank(s_found, tid / 3)[tid % 3] = tid % 3 == 0 ? prefix : tid % 3 == 1 ? (uint32_t)want : ties;
+  if (listed) {
+    uint32_t* list = cluster.map_shared_rank(s_list, 0);
+    int* end = cluster.map_shared_rank(&s_listed, 0);
+    each([&](int, uint32_t k, bool in) {
+      const bool counts = in && (k & mask) == prefix;
+      const unsigned m = __ballot_sync(0xffffffffu, counts);
+      if (m == 0) return;
+      int at = 0;
+      if (lane == __ffs(m) - 1) at = atomicAdd(end, __popc(m));
+      at = __shfl_sync(0xffffffffu, at, __ffs(m) - 1) + __popc(m & ((1u << lane) - 1u));
+      if (counts) list[at] = k;
+    });
+    sync();
+    if (rank == 0) {
+#pragma unroll 1
+      for (; pass < 3 && in_bin != want; pass++) {
+        const uint32_t low = pass < 2 ? 2047u : 1023u;
+        for (int j0 = warp * 32; j0 < s_listed; j0 += SEL_THREADS) {
+          const int j = j0 + lane;
+          const uint32_t k = j < s_listed ? s_list[j] : 0u;
+          count(s_hist[pass], k, j < s_listed && (k & mask) == prefix, sh, low);
+        }
+        __syncthreads();
+        find(s_hist[pass], 1);
+        __syncthreads();
+        take(sh, low);
+        sh = pass == 0 ? 10 : 0;
+        __syncthreads();
+      }
+      if (tid < S) {
+        int* to = cluster.map_shared_rank(s_found, tid);
+        to[0] = (int)prefix;
+        to[1] = want;
+        to[2] = in_bin;
+      }
+    }
+    sync();
+    prefix = (uint32_t)s_found[0];
+    want = s_found[1];
+    in_bin = s_found[2];
   }
-  sync();
-  prefix = s_found[0];
-  want = (int)s_found[1];
-  ties = s_found[2];
+  const bool ties = in_bin != want;   // else all of them are kept: every key >= prefix
 
   // the CTAs' counts of one quantity, told to the cluster; the sum over the CTAs before this one
   auto before_cta = [&](int which) {
@@ -1072,7 +1130,8 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const Evict a, int ctas
   const int64_t b = blockIdx.x / ctas;
   const int part = (int)(blockIdx.x % ctas);
   const int H = a.c.H, shift = a.c.ps_shift, ps = 1 << shift, sub = threadIdx.x % LPR;
-  const int64_t items = a.count[b] * H;
+  // items in the order (32 moves, head, move): neighbours then share a page's part of a head
+  const int64_t count = a.count[b], items = (count + 31) / 32 * 32 * H;
   const int64_t *tos = a.to + b * a.moves, *froms = a.from + b * a.moves;
   uint4 *k = static_cast<uint4*>(a.c.k), *v = static_cast<uint4*>(a.c.v);
   for (int64_t x0 = (int64_t)part * R * U + threadIdx.x / LPR; x0 < items; x0 += (int64_t)ctas * R * U) {
@@ -1081,11 +1140,10 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const Evict a, int ctas
     int h[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int64_t x = x0 + u * R;
+      const int64_t x = x0 + u * R, group = x / 32, c = group / H, m = c * 32 + x % 32;
       rt[u] = -1;
-      if (x >= items) continue;
-      const int64_t m = x / H;
-      h[u] = (int)(x - m * H);
+      if (x >= items || m >= count) continue;
+      h[u] = (int)(group - c * H);
       to[u] = tos[m];
       from[u] = froms[m];
       if (to[u] < 0 || from[u] < 0) continue;
@@ -1188,26 +1246,21 @@ inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaSt
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // as many CTAs as hold the keys of a row's slots in registers, at most 8
+  // as many CTAs as hold the keys of a row's slots in registers, and more while there are SMs for
+  // them, at most 8
   int S = 1;
-  while (S < SEL_CLUSTER && (int64_t)S * SEL_THREADS * SEL_KEYS < a.room) S *= 2;
-  const int smem = a.room <= SEL_SMEM_KEYS ? (int)a.room * 4 : 0;
-  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           SEL_SMEM_KEYS * 4) != cudaSuccess)
-    return HSTU_ERR_CUDA;
+  while (S < SEL_CLUSTER && ((int64_t)S * SEL_THREADS * SEL_KEYS < a.room || 2 * S * a.B <= sms)) S *= 2;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = S;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(a.B * S));
   cfg.blockDim = dim3(SEL_THREADS);
-  cfg.dynamicSmemBytes = smem;
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess) return HSTU_ERR_CUDA;
   hstu_status_t rc = launched();
   if (rc != HSTU_OK) return rc;
   // eight CTAs a SM over all sequences, at least one each
   int64_t ctas = (8LL * sms + a.B - 1) / a.B;
   attr[0] = cudaLaunchAttribute{};
-  cfg.dynamicSmemBytes = 0;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its launch overlaps the selection
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)(a.B * ctas));
