@@ -469,8 +469,8 @@ PagedWorkspace paged_layout(const hstu_shape_t& s, void* base) {
 }
 
 struct EvictWorkspace {
-  uint32_t* keys;
-  int64_t *to, *from, *count;
+  uint32_t *keys, *to, *from;
+  int64_t* count;
   int64_t moves;
   size_t total;
 };
@@ -484,10 +484,10 @@ EvictWorkspace evict_layout(int64_t B, int64_t room, void* base) {
   char* b = static_cast<char*>(base);
   w.keys = b ? reinterpret_cast<uint32_t*>(b + o) : nullptr;
   o += align_up((size_t)B * room * sizeof(uint32_t));
-  w.to = b ? reinterpret_cast<int64_t*>(b + o) : nullptr;
-  o += align_up((size_t)B * w.moves * sizeof(int64_t));
-  w.from = b ? reinterpret_cast<int64_t*>(b + o) : nullptr;
-  o += align_up((size_t)B * w.moves * sizeof(int64_t));
+  w.to = b ? reinterpret_cast<uint32_t*>(b + o) : nullptr;
+  o += align_up((size_t)B * w.moves * sizeof(uint32_t));
+  w.from = b ? reinterpret_cast<uint32_t*>(b + o) : nullptr;
+  o += align_up((size_t)B * w.moves * sizeof(uint32_t));
   w.count = b ? reinterpret_cast<int64_t*>(b + o) : nullptr;
   o += align_up((size_t)B * sizeof(int64_t));
   w.total = o;

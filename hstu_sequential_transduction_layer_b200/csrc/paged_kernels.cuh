@@ -77,6 +77,11 @@ __device__ __forceinline__ int time_bucket(int64_t dt, int Tb) {
   return b < Tb ? b : Tb - 1;
 }
 
+// a / b for 0 <= a, 0 < b; the 64-bit division takes several times as long as the 32-bit one.
+__device__ __forceinline__ int64_t div_by(int64_t a, int b) {
+  return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // 16 bytes of T as pairs of fp32.
 template <typename T> struct vec16;
 template <> struct vec16<float> {
@@ -793,7 +798,7 @@ struct Evict {
   int64_t* new_lens;
   // workspace
   uint32_t* keys;            // [B, room]
-  int64_t *to, *from;        // [B, moves]: flat slots (page * page_size + offset)
+  uint32_t *to, *from;       // [B, moves]: slots of the pool (page * page_size + offset), or ~0: none
   int64_t* count;            // [B]
   int64_t room, moves;
 };
@@ -819,7 +824,7 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
 // the mantissa) spread accumulated weights over enough bins that the shared-memory atomics seldom
 // meet; warps whose keys all fall into one bin add them at once.  Bound by latency, some ten
 // dependent steps, and by the instructions of code that runs once: few warps, and several CTAs.
-constexpr int SEL_THREADS = 256, SEL_WARPS = SEL_THREADS / 32, SEL_KEYS = 8, SEL_CLUSTER = 8;
+constexpr int SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32, SEL_KEYS = 8, SEL_CLUSTER = 8;
 constexpr int SEL_BINS = 2048, SEL_LIST = 1024;
 
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a) {
@@ -858,9 +863,11 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   if (tid == 0) s_listed = 0;
   for (int i = tid; i < 3 * SEL_BINS / 4; i += SEL_THREADS)
     reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
+  if (S > 1) cluster.barrier_arrive(); else __syncthreads();
 
   // scores: the loads of SEL_KEYS slots and four heads are in flight at once
-  uint32_t key[SEL_KEYS];
+  // (unconditional, from some slot where there is none: a load under a condition is waited for at once)
+  uint32_t key[SEL_KEYS], page[SEL_KEYS];
 #pragma unroll 1
   for (int r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
     uint32_t at[SEL_KEYS];      // rows of weights: below 2^32
@@ -870,7 +877,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
 #pragma unroll
     for (int i = 0; i < SEL_KEYS; i++) {
       const int j = start + (r0 + i) * 32;
-      at[i] = r0 + i < rounds && j < n ? (uint32_t)pages[j >> shift] : 0u;
+      at[i] = (uint32_t)pages[(j < n ? j : n - 1) >> shift];
       sum[i] = 0.0;
     }
 #pragma unroll
@@ -880,7 +887,8 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
         if (at[i] < (uint32_t)a.c.num_pages) live |= 1u << i;
         else report(HSTU_ERR_DEVICE_BAD_OFFSETS);
       }
-      if (!(live >> i & 1)) at[i] = 0;   // any slot: the value is dropped
+      if (r0 == 0) page[i] = live >> i & 1 ? at[i] : ~0u;
+      if (!(live >> i & 1)) at[i] = 0;   // any page: the value is dropped
       const int o = j & (ps - 1);
       pos[i] = a.c.positions[((int64_t)at[i] << shift) + o];
       at[i] = ((at[i] * (uint32_t)H) << shift) + o;
@@ -902,23 +910,32 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
     for (int i = 0; i < SEL_KEYS; i++) {
       const int j = start + (r0 + i) * 32;
       uint32_t k = (int64_t)pos[i] >= oldest ? KEY_RECENT : weight_key((float)sum[i]);
-      if (!(live >> i & 1)) k = 0;
+      if (!(live >> i & 1)) k = 0;         // a slot of no page goes first, and nothing moves for it
       if (r0 == 0) key[i] = k;
       else if (r0 + i < rounds && j < n) spill[j] = k;
     }
   }
-  // f(slot, key, whether there is such a slot) for the warp's slots in order; all lanes take part
-  auto each = [&](auto f) {
+  // f(slot, key, its page or some page, whether there is such a slot) for the warp's slots in order;
+  // all lanes take part
+  auto each = [&](auto f, bool pages_too = false) {
 #pragma unroll
     for (int i = 0; i < SEL_KEYS; i++)
-      if (i < rounds) f(start + i * 32, key[i], start + i * 32 < n);
+      if (i < rounds) f(start + i * 32, key[i], page[i], start + i * 32 < n);
 #pragma unroll 1
-    for (int r = SEL_KEYS; r < rounds; r++) {
-      const int j = start + r * 32;
-      f(j, j < n ? spill[j] : 0u, j < n);
+    for (int r0 = SEL_KEYS; r0 < rounds; r0 += SEL_KEYS) {
+      uint32_t k[SEL_KEYS], pg[SEL_KEYS];
+#pragma unroll
+      for (int i = 0; i < SEL_KEYS; i++) {
+        const int j = start + (r0 + i) * 32, at = j < n ? j : n - 1;
+        k[i] = spill[at];
+        pg[i] = pages_too ? (uint32_t)pages[at >> shift] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < SEL_KEYS; i++)
+        if (r0 + i < rounds) f(start + (r0 + i) * 32, k[i], pg[i], start + (r0 + i) * 32 < n);
     }
   };
-  sync();   // bins are zero everywhere
+  if (S > 1) cluster.barrier_wait();   // bins are zero everywhere
 
   uint32_t prefix = 0, mask = 0;
   int want = budget;          // of the keys that share the prefix, how many are kept
@@ -990,13 +1007,18 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       listed = true;
       break;
     }
-    each([&](int, uint32_t k, bool in) { count(hist, k, in && (k & mask) == prefix, sh, low); });
+    each([&](int, uint32_t k, uint32_t, bool in) { count(hist, k, in && (k & mask) == prefix, sh, low); });
     __syncthreads();
     if (S > 1) {
       int* to = cluster.map_shared_rank(hist, 0);
       if (rank > 0)
-        for (int i = tid; i < SEL_BINS; i += SEL_THREADS)
-          if (hist[i]) atomicAdd(to + i, hist[i]);
+        for (int i = tid * 4; i < SEL_BINS; i += SEL_THREADS * 4) {
+          const int4 x = *reinterpret_cast<const int4*>(hist + i);
+          if (x.x) atomicAdd(to + i, x.x);
+          if (x.y) atomicAdd(to + i + 1, x.y);
+          if (x.z) atomicAdd(to + i + 2, x.z);
+          if (x.w) atomicAdd(to + i + 3, x.w);
+        }
       cluster.sync();
     }
     if (rank == 0) find(hist, S);
@@ -1008,7 +1030,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   if (listed) {
     uint32_t* list = cluster.map_shared_rank(s_list, 0);
     int* end = cluster.map_shared_rank(&s_listed, 0);
-    each([&](int, uint32_t k, bool in) {
+    each([&](int, uint32_t k, uint32_t, bool in) {
       const bool counts = in && (k & mask) == prefix;
       const unsigned m = __ballot_sync(0xffffffffu, counts);
       if (m == 0) return;
@@ -1060,7 +1082,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   int equal = 0;              // with ties: equal keys in slots before the warp's
   if (ties) {
     int cnt = 0;
-    each([&](int, uint32_t k, bool in) { cnt += __popc(__ballot_sync(0xffffffffu, in && k == prefix)); });
+    each([&](int, uint32_t k, uint32_t, bool in) { cnt += __popc(__ballot_sync(0xffffffffu, in && k == prefix)); });
     if (lane == 0) s_warp[warp] = cnt;
     __syncthreads();
     const int w = lane < SEL_WARPS ? s_warp[lane] : 0;
@@ -1069,25 +1091,25 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
     sync();
     equal += before_cta(0);
   }
-  // f(slot, lanes whose slot is a gap, lanes whose slot moves) for the warp's slots in order
-  auto each_flagged = [&](auto f) {
+  // f(slot, its page, lanes whose slot is a gap, lanes whose slot moves) for the warp's slots in order
+  auto each_flagged = [&](auto f, bool pages_too) {
     int seen = equal;
-    each([&](int j, uint32_t k, bool in) {
+    each([&](int j, uint32_t k, uint32_t pg, bool in) {
       bool keep = in && k >= prefix;
       if (ties) {
         const unsigned same = __ballot_sync(0xffffffffu, in && k == prefix);
         keep = in && (k > prefix || (k == prefix && seen + __popc(same & ((1u << lane) - 1u)) < want));
         seen += __popc(same);
       }
-      f(j, __ballot_sync(0xffffffffu, in && j < budget && !keep),
+      f(j, k, pg, __ballot_sync(0xffffffffu, in && j < budget && !keep),
         __ballot_sync(0xffffffffu, in && j >= budget && keep));
-    });
+    }, pages_too);
   };
   int gaps = 0, movers = 0;
-  each_flagged([&](int, unsigned g, unsigned m) {
+  each_flagged([&](int, uint32_t, uint32_t, unsigned g, unsigned m) {
     gaps += __popc(g);
     movers += __popc(m);
-  });
+  }, false);
   if (lane == 0) {
     s_gaps[warp] = gaps;
     s_movers[warp] = movers;
@@ -1107,64 +1129,74 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
     a.count[b] = all;         // as many gaps below the budget as kept slots from there on
     a.new_lens[b] = budget;
   }
-  each_flagged([&](int j, unsigned g, unsigned m) {
+  each_flagged([&](int j, uint32_t, uint32_t pg, unsigned g, unsigned m) {
     const unsigned bit = 1u << lane;
     if ((g | m) & bit) {
-      const int64_t pg = page_of(pages, j >> shift, a.c.num_pages);
-      const int64_t flat = pg < 0 ? -1 : (pg << shift) + (j & (ps - 1));
+      const uint32_t flat = pg < (uint32_t)a.c.num_pages ? (pg << shift) + (j & (ps - 1)) : ~0u;
       if (g & bit) a.to[b * a.moves + gap_at + __popc(g & (bit - 1u))] = flat;
       else a.from[b * a.moves + mover_at + __popc(m & (bit - 1u))] = flat;
     }
     gap_at += __popc(g);
     mover_at += __popc(m);
-  });
-  if (S > 1) cluster.sync();   // no CTA leaves while another may read or write its shared memory
+  }, true);
+  // (nobody has touched another CTA's shared memory since the last sync: each may leave)
 }
 
 // Moves the kept rows into the gaps.  Sources lie at or above slot `budget`, destinations below it,
-// so rows move in any order.  LPR lanes of 16 bytes a (token, head), K and V; HBM-bound.
+// so rows move in any order.  LPR lanes of 16 bytes a (token, head), K and V; rows are taken in the
+// order (32 moves, head, move), so that neighbours share a page's part of a head.  HBM-bound, on
+// pieces of 128 bytes or more in no order.
 template <int LPR>
-__global__ void __launch_bounds__(256) evict_move_kernel(const Evict a, int ctas) {
+__global__ void __launch_bounds__(256, 4) evict_move_kernel(const Evict a, int ctas) {
   constexpr int R = 256 / LPR, U = 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t b = blockIdx.x / ctas;
-  const int part = (int)(blockIdx.x % ctas);
-  const int H = a.c.H, shift = a.c.ps_shift, ps = 1 << shift, sub = threadIdx.x % LPR;
-  // items in the order (32 moves, head, move): neighbours then share a page's part of a head
+  const int part = (int)(blockIdx.x % ctas), H = a.c.H, shift = a.c.ps_shift, ps = 1 << shift;
+  const int sub = threadIdx.x % LPR;
   const int64_t count = a.count[b], items = (count + 31) / 32 * 32 * H;
-  const int64_t *tos = a.to + b * a.moves, *froms = a.from + b * a.moves;
-  uint4 *k = static_cast<uint4*>(a.c.k), *v = static_cast<uint4*>(a.c.v);
+  const uint32_t *tos = a.to + b * a.moves, *froms = a.from + b * a.moves;
+  uint4 *k = static_cast<uint4*>(a.c.k) + sub, *v = static_cast<uint4*>(a.c.v) + sub;
   for (int64_t x0 = (int64_t)part * R * U + threadIdx.x / LPR; x0 < items; x0 += (int64_t)ctas * R * U) {
     uint4 kr[U], vr[U];
-    int64_t rt[U], rf[U], to[U], from[U];
-    int h[U];
+    uint32_t to[U], from[U];   // slots, then rows
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int64_t x = x0 + u * R, group = x / 32, c = group / H, m = c * 32 + x % 32;
-      rt[u] = -1;
-      if (x >= items || m >= count) continue;
-      h[u] = (int)(group - c * H);
-      to[u] = tos[m];
-      from[u] = froms[m];
-      if (to[u] < 0 || from[u] < 0) continue;
-      rt[u] = ((((to[u] >> shift) * H + h[u]) << shift) + (to[u] & (ps - 1)));
-      rf[u] = ((((from[u] >> shift) * H + h[u]) << shift) + (from[u] & (ps - 1)));
-      kr[u] = k[rf[u] * LPR + sub];
-      vr[u] = v[rf[u] * LPR + sub];
-    }
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      if (rt[u] < 0) continue;
-      k[rt[u] * LPR + sub] = kr[u];
-      v[rt[u] * LPR + sub] = vr[u];
-      if (sub == 0) {
-        a.c.weights[rt[u]] = a.c.weights[rf[u]];
-        if (h[u] == 0) {
-          a.c.positions[to[u]] = a.c.positions[from[u]];
-          if (a.c.timestamps) a.c.timestamps[to[u]] = a.c.timestamps[from[u]];
-        }
+      const int64_t x = x0 + u * R, m = div_by(x / 32, H) * 32 + x % 32;
+      to[u] = from[u] = ~0u;
+      if (x < items && m < count) {
+        to[u] = tos[m];
+        from[u] = froms[m];
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t g = (x0 + u * R) / 32;
+      const uint32_t h = (uint32_t)(g - div_by(g, H) * H);
+      if (to[u] == ~0u || from[u] == ~0u) {
+        to[u] = ~0u;
+        continue;
+      }
+      const uint32_t t = to[u], f = from[u];
+      to[u] = ((t >> shift) * H + h << shift) + (t & (ps - 1));
+      from[u] = ((f >> shift) * H + h << shift) + (f & (ps - 1));
+      if (h == 0 && sub == 0) {
+        a.c.positions[t] = a.c.positions[f];
+        if (a.c.timestamps) a.c.timestamps[t] = a.c.timestamps[f];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      if (to[u] != ~0u) {
+        kr[u] = __ldcs(k + (int64_t)from[u] * LPR);
+        vr[u] = __ldcs(v + (int64_t)from[u] * LPR);
+        if (sub == 0) a.c.weights[to[u]] = a.c.weights[from[u]];
+      }
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      if (to[u] != ~0u) {
+        k[(int64_t)to[u] * LPR] = kr[u];
+        v[(int64_t)to[u] * LPR] = vr[u];
+      }
   }
 }
 
@@ -1258,7 +1290,7 @@ inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaSt
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess) return HSTU_ERR_CUDA;
   hstu_status_t rc = launched();
   if (rc != HSTU_OK) return rc;
-  // eight CTAs a SM over all sequences, at least one each
+  // twice what fits the SMs at once, over all sequences; at least one each
   int64_t ctas = (8LL * sms + a.B - 1) / a.B;
   attr[0] = cudaLaunchAttribute{};
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its launch overlaps the selection
