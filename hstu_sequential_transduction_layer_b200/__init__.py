@@ -360,27 +360,29 @@ def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, device):
     """Address of a tensor argument of the paged cache's calls, checked; None for None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of {numel} elements on {device} is "
-                         f"wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.device == device:
+        return t.data_ptr()
+    raise ValueError(f"{name}: a contiguous {dtype} tensor of {numel} elements on {device} is wanted, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-class _on:
-    """Makes `device` current for a call (kernels launch on the current device)."""
-
-    def __init__(self, device):
-        self._d, self._back = device.index, -1
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self._d:
-            torch.cuda.set_device(self._d)
-            self._back = now
-
-    def __exit__(self, *exc):
-        if self._back >= 0:
-            torch.cuda.set_device(self._back)
+def _call(fn, what: str, device, stream, *args) -> None:
+    """Calls a library function with `device` current (kernels launch on the current device), on
+    `stream` or that device's current stream."""
+    index = device.index
+    if stream is None:
+        # the address alone: building a torch.cuda.Stream takes longer than the launch
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    now = torch.cuda.current_device()
+    if now == index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != HSTU_OK:
+        raise HstuError(rc, what)
 
 
 def _table(cache: PagedCache, page_table, cache_lens, next_positions):
@@ -419,9 +421,8 @@ def hstu_cache_append(cache: PagedCache, uvqk, seq_offsets, timestamps, page_tab
     up = _arg("uvqk", uvqk, cache.k.dtype, T * n1, dev)
     op = _arg("seq_offsets", seq_offsets, torch.int64, B + 1, dev)
     sp = _arg("timestamps", timestamps, torch.int64, T, dev)
-    with _on(dev):
-        _check(_lib.hstu_cache_append(cache.ref, B, T, up, op, sp, tp, M, lp, np_,
-                                      _stream(stream)), "hstu_cache_append")
+    _call(_lib.hstu_cache_append, "hstu_cache_append", dev, stream, cache.ref, B, T, up, op, sp, tp,
+          M, lp, np_)
 
 
 def paged_attention_workspace_size(shape: HstuShape) -> int:
@@ -442,11 +443,9 @@ def hstu_paged_attention_fwd(shape: HstuShape, cache: PagedCache, uvqk, page_tab
     ap = _arg("av", av, torch.float32, B * w, dev)
     pos, tim, ali = _biases(shape, pos_table, time_table, alibi_slopes, dev)
     ws = _space(workspace, lambda: paged_attention_workspace_size(shape), dev)
-    with _on(dev):
-        _check(_lib.hstu_paged_attention_fwd(
-            ctypes.byref(shape), cache.ref, up, tp, M, lp, np_, sp, pos, tim, ali, scale,
-            1 if append else 0, ap, ws.data_ptr(), ws.nbytes, _stream(stream)),
-            "hstu_paged_attention_fwd")
+    _call(_lib.hstu_paged_attention_fwd, "hstu_paged_attention_fwd", dev, stream, ctypes.byref(shape),
+          cache.ref, up, tp, M, lp, np_, sp, pos, tim, ali, scale, 1 if append else 0, ap,
+          ws.data_ptr(), ws.nbytes)
     return av
 
 
@@ -465,7 +464,7 @@ def hstu_paged_layer_fwd(shape: HstuShape, cache: PagedCache, X, page_table, cac
         raise ValueError(f"page_table has {B} rows, the shape {shape.num_seqs} sequences")
     if out is None:
         out = torch.empty_like(X)
-    args = [_arg("X", X, dt, B * d, dev)]
+    xp = _arg("X", X, dt, B * d, dev)
     weights = [_arg("W1", W1, dt, d * 4 * w, dev), _arg("b1", b1, dt, 4 * w, dev),
                _arg("W2", W2, dt, w * d, dev), _arg("b2", b2, dt, d, dev),
                _arg("ln_w", ln_w, dt, w, dev), _arg("ln_b", ln_b, dt, w, dev)]
@@ -473,11 +472,9 @@ def hstu_paged_layer_fwd(shape: HstuShape, cache: PagedCache, X, page_table, cac
     pos, tim, ali = _biases(shape, pos_table, time_table, alibi_slopes, dev)
     op = _arg("out", out, dt, B * d, dev)
     ws = _space(workspace, lambda: paged_layer_workspace_size(shape), dev)
-    with _on(dev):
-        _check(_lib.hstu_paged_layer_fwd(
-            ctypes.byref(shape), cache.ref, *args, tp, M, lp, np_, sp, *weights, pos, tim, ali,
-            float(scale), 1 if append else 0, op, ws.data_ptr(), ws.nbytes, _stream(stream)),
-            "hstu_paged_layer_fwd")
+    _call(_lib.hstu_paged_layer_fwd, "hstu_paged_layer_fwd", dev, stream, ctypes.byref(shape),
+          cache.ref, xp, tp, M, lp, np_, sp, *weights, pos, tim, ali, scale, 1 if append else 0, op,
+          ws.data_ptr(), ws.nbytes)
     return out
 
 
@@ -495,10 +492,8 @@ def hstu_cache_evict(cache: PagedCache, page_table, cache_lens, next_positions, 
         new_lens = torch.empty_like(cache_lens)
     ep = _arg("new_lens", new_lens, torch.int64, B, dev)
     ws = _space(workspace, lambda: cache_evict_workspace_size(cache, B, M), dev)
-    with _on(dev):
-        _check(_lib.hstu_cache_evict(cache.ref, B, tp, M, lp, np_, budget, recent, ep,
-                                     ws.data_ptr(), ws.nbytes, _stream(stream)),
-               "hstu_cache_evict")
+    _call(_lib.hstu_cache_evict, "hstu_cache_evict", dev, stream, cache.ref, B, tp, M, lp, np_, budget,
+          recent, ep, ws.data_ptr(), ws.nbytes)
     return new_lens
 
 
