@@ -360,7 +360,7 @@ def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, device):
     """Address of a tensor argument of the paged cache's calls, checked; None for None."""
     if t is None:
         return None
-    if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.device == device:
+    if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.get_device() == device.index:
         return t.data_ptr()
     raise ValueError(f"{name}: a contiguous {dtype} tensor of {numel} elements on {device} is wanted, "
                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")

@@ -1080,7 +1080,6 @@ hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seq
   if (cache->timestamps && !timestamps) return HSTU_ERR_INVALID_ARG;
   if (overlaps_cache(uvqk, (size_t)total_tokens * 4 * cache->num_heads * row_bytes(*cache), *cache))
     return HSTU_ERR_INVALID_ARG;
-  if (total_tokens / paged::APPEND_TOKENS >= (1LL << 31) - 1) return HSTU_ERR_UNSUPPORTED;
   return paged::launch_append(cache_view(*cache), row_bytes(*cache), total_tokens, num_seqs, uvqk,
                               seq_offsets, timestamps, page_table, max_pages, cache_lens,
                               next_positions, static_cast<cudaStream_t>(stream));

@@ -116,10 +116,12 @@ template <> struct vec16<bf16> {
 // one tile ahead.  A warp that holds all tiles of a (sequence, head) writes its row of AV; parts
 // are joined first among the CTA's warps in shared memory, then, where a (sequence, head) spans
 // CTAs, by a second kernel, always in the same order.
-constexpr int ATTN_WARPS = 12;                  // consumers
+constexpr int ATTN_WARPS = 11;                  // consumers
 constexpr int ATTN_STAGES = 2;
 constexpr int ATTN_INFOS = 4;                   // tiles told of: two in flight and two ahead
+static_assert(ATTN_STAGES == 2 && ATTN_INFOS == ATTN_STAGES + 2, "the start tells of and fills two stages");
 constexpr int ATTN_THREADS = (ATTN_WARPS + 1) * 32;
+constexpr int ATTN_NAP = 30;                   // ns between the producer's looks for work
 constexpr int ATTN_HALF = 4096;                 // bytes of a tile's K, and of its V
 // CTAs of the attention: one a SM, at most this many (the workspace holds a part record for each).
 constexpr int ATTN_MAX_CTAS = 256;
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
   unsigned char* smem = smem_raw + ((128 - (sm100::smem_u32(smem_raw) & 127)) & 127);
   float(*sp)[2][HD] = reinterpret_cast<float(*)[2][HD]>(smem + Cfg::PARTS);
   __shared__ int pre[ATTN_THREADS], s_len[ATTN_THREADS];
-  __shared__ int scratch[ATTN_WARPS + 1];
+  __shared__ int scratch[ATTN_THREADS / 32];
   __shared__ int s_before[ATTN_WARPS], s_pair[ATTN_WARPS];
   __shared__ TileInfo s_info[ATTN_WARPS][ATTN_INFOS];
   __shared__ int s_issued[ATTN_WARPS];   // tiles whose TileInfo is written
@@ -257,13 +259,41 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < ATTN_WARPS; w++) x += w < warp ? scratch[w] : 0;
+    for (int w = 0; w < ATTN_THREADS / 32; w++) x += w < warp ? scratch[w] : 0;
     pre[threadIdx.x] = x;
     __syncthreads();
   }
   // every consumer's share: `share` tiles, one more for the first `over` of them
   const uint32_t units = (uint32_t)pre[ATTN_THREADS - 1] * H, W = gridDim.x * ATTN_WARPS;
   const uint32_t share = units / W, over = units - share * W;
+
+  // copies the cached rows of tile k into consumer c's ring; its barrier completes once it is also
+  // arrived on
+  auto fill = [&](int c, int k) {
+    const int stage = k % ATTN_STAGES;
+    const TileInfo& t = s_info[c][k % ATTN_INFOS];
+    uint64_t* bar = &full_bar[c][stage];
+    unsigned char* dst = smem + (c * ATTN_STAGES + stage) * STAGE;
+    int rows[NP], sum = 0;
+#pragma unroll
+    for (int p = 0; p < NP; p++) {
+      const int left = t.left - PIECE * p;
+      rows[p] = left <= 0 || (t.flags & (2 << p)) ? 0 : (left < PIECE ? left : PIECE);
+      sum += rows[p];
+    }
+    sm100::mbar_expect_tx(bar, (uint32_t)sum * 2 * ROW);
+    if (NP > 1 && ps >= TILE) {   // one page
+      rows[0] = sum;
+      rows[NP - 1] = 0;
+    }
+#pragma unroll
+    for (int p = 0; p < NP; p++) {
+      if (rows[p] == 0) continue;
+      const int64_t at = t.row[p] * HD;
+      bulk_load(dst + p * PIECE * ROW, static_cast<const T*>(a.c.k) + at, rows[p] * ROW, bar);
+      bulk_load(dst + ATTN_HALF + p * PIECE * ROW, static_cast<const T*>(a.c.v) + at, rows[p] * ROW, bar);
+    }
+  };
 
   int done = 0;   // tiles taken
   if (warp == ATTN_WARPS) {
@@ -356,61 +386,35 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
         pages();
       }
     };
-    // copies the cached rows of tile k; its barrier completes once it is also arrived on
-    auto fill = [&](int k) {
-      const int stage = k % ATTN_STAGES;
-      const TileInfo& t = s_info[lane][k % ATTN_INFOS];
-      uint64_t* bar = &full_bar[lane][stage];
-      unsigned char* dst = smem + (lane * ATTN_STAGES + stage) * STAGE;
-      int rows[NP], sum = 0;
-#pragma unroll
-      for (int p = 0; p < NP; p++) {
-        const int left = t.left - PIECE * p;
-        rows[p] = left <= 0 || (t.flags & (2 << p)) ? 0 : (left < PIECE ? left : PIECE);
-        sum += rows[p];
-      }
-      sm100::mbar_expect_tx(bar, (uint32_t)sum * 2 * ROW);
-      if (NP > 1 && ps >= TILE) {   // one page
-        rows[0] = sum;
-        rows[NP - 1] = 0;
-      }
-#pragma unroll
-      for (int p = 0; p < NP; p++) {
-        if (rows[p] == 0) continue;
-        const int64_t at = t.row[p] * HD;
-        bulk_load(dst + p * PIECE * ROW, static_cast<const T*>(a.c.k) + at, rows[p] * ROW, bar);
-        bulk_load(dst + ATTN_HALF + p * PIECE * ROW, static_cast<const T*>(a.c.v) + at, rows[p] * ROW, bar);
-      }
-    };
-    // A consumer that has seen tile k's barrier complete has been told of tiles k + 1 and k + 2: the
-    // arrival comes after.
-    if (count > 0) tell();
-    if (count > 0) fill(0);
-    if (count > 1) tell();
-    if (count > 1) fill(1);
-    for (; done < 2 && done < count; done++) {
+    // The consumers fill their first ATTN_STAGES tiles themselves (a warp's copies are issued one lane
+    // after another).  From then on a consumer that has seen tile k's barrier complete has been told
+    // of tiles k + 1 and k + 2: the arrival comes after.
+    for (int k = 0; k < ATTN_STAGES + 2; k++)
       if (told < count) tell();
-      sm100::mbar_arrive(&full_bar[lane][done]);
-    }
-    uint64_t idle = 0;
+    done = count < ATTN_STAGES ? count : ATTN_STAGES;
+    uint64_t idle = 0;   // since when no lane had anything to refill
     while (__any_sync(0xffffffffu, done < count)) {
       const int stage = done % ATTN_STAGES;
-      if (done < count && mbar_test(&free_bar[lane][stage], (done / ATTN_STAGES + 1) & 1)) {
-        fill(done);
+      const bool go = done < count && mbar_test(&free_bar[lane][stage], (done / ATTN_STAGES + 1) & 1);
+      if (go) {
+        fill(lane, done);
         if (told < count) tell();
         sm100::mbar_arrive(&full_bar[lane][stage]);
         done++;
+      }
+      if (__any_sync(0xffffffffu, go)) {
         idle = 0;
-      } else if (done < count) {
-        // nothing to refill yet: bounded, as every wait of this kernel
-        const uint64_t now = sm100::globaltimer();
-        if (idle == 0) idle = now;
-        if (now - idle > 2 * sm100::kWaitLimitNs) {
-          s_abort = 1;
-          report(HSTU_ERR_DEVICE_TIMEOUT);
-        }
+        continue;
+      }
+      // bounded, as every wait of this kernel; asleep, so as to leave the issue slots to the consumers
+      const uint64_t now = sm100::globaltimer();
+      if (idle == 0) idle = now;
+      if (lane == 0 && now - idle > 2 * sm100::kWaitLimitNs) {
+        s_abort = 1;
+        report(HSTU_ERR_DEVICE_TIMEOUT);
       }
       if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort))) break;
+      __nanosleep(ATTN_NAP);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   } else {
@@ -482,11 +486,21 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
     for (int e = 0; e < E / 2; e++) acc[e] = 0;
     bool whole = true, ok = true;   // whole: acc holds the (sequence, head) from its first tile on
     if (count > 0 && (ok = await(0))) {
+      if (lane == 0) {
+        fill(warp, 0);
+        sm100::mbar_arrive(&full_bar[warp][0]);
+      }
       whole = told_of(0).flags & 1;
       q = new_row(told_of(0), 2);
       look_ahead(0);
       copy_async_commit();
-      if (count > 1 && (ok = await(1))) look_ahead(1);
+      if (count > 1 && (ok = await(1))) {
+        if (lane == 0) {
+          fill(warp, 1);
+          sm100::mbar_arrive(&full_bar[warp][1]);
+        }
+        look_ahead(1);
+      }
       copy_async_commit();
       copy_async_wait<1>();
       look_up(0);
@@ -506,7 +520,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
       ok = sm100::mbar_wait(&full_bar[warp][stage], (done / ATTN_STAGES) & 1, &s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (done + 2 < count) look_ahead(done + 2);
+      if (done + 2 < count) {
+        if (done < ATTN_STAGES && !(ok = await(done + 2))) break;
+        look_ahead(done + 2);
+      }
       copy_async_commit();
       const uint4* ks = reinterpret_cast<const uint4*>(src) + lane;
       const uint4* vs = ks + ATTN_HALF / 16;
@@ -706,12 +723,12 @@ __global__ void __launch_bounds__(ATTN_MAX_CTAS) attention_join_kernel(float* av
 }
 
 // Rows of a jagged U|V|Q|K batch into the cache: token t of sequence b goes to slot lens[b] + (t -
-// off[b]).  A CTA takes APPEND_TOKENS tokens: a thread a token finds its sequence by bisection and its
+// off[b]).  A CTA takes `tokens` tokens: a thread a token finds its sequence by bisection and its
 // row's place, then all threads copy, 16 bytes at a time; K and V rows are read in order, 1 to 8 KB a
 // token, and written as the heads' separate rows of 128 bytes or more.  HBM-bound.
-constexpr int APPEND_TOKENS = 16;
+constexpr int APPEND_TOKENS = 32, APPEND_PIECES = 1024;
 template <int LPR>
-__global__ void __launch_bounds__(256) append_kernel(const Cache c, int64_t Tn, int64_t B,
+__global__ void __launch_bounds__(256) append_kernel(const Cache c, int tokens, int64_t Tn, int64_t B,
                                                      const uint4* __restrict__ uvqk,
                                                      const int64_t* __restrict__ off,
                                                      const int64_t* __restrict__ ts,
@@ -726,9 +743,9 @@ __global__ void __launch_bounds__(256) append_kernel(const Cache c, int64_t Tn, 
     if ((s == 0 && v != 0) || (s == B && v != Tn) || v < 0 || v > Tn || (s > 0 && off[s - 1] > v))
       report(HSTU_ERR_DEVICE_BAD_OFFSETS);
   }
-  const int64_t t0 = (int64_t)blockIdx.x * APPEND_TOKENS;
+  const int64_t t0 = (int64_t)blockIdx.x * tokens;
   const int shift = c.ps_shift, ps = 1 << shift, H = c.H;
-  if (threadIdx.x < APPEND_TOKENS) {
+  if (threadIdx.x < tokens) {
     const int64_t t = t0 + threadIdx.x;
     int64_t row = -1;
     if (t < Tn && t >= off[0] && t < off[B]) {
@@ -754,7 +771,7 @@ __global__ void __launch_bounds__(256) append_kernel(const Cache c, int64_t Tn, 
   }
   __syncthreads();
   // piece x of a token: 16 bytes of K and of V; head x / LPR
-  const int width = H * LPR, total = APPEND_TOKENS * width;
+  const int width = H * LPR, total = tokens * width;
   constexpr int U = 4;
   for (int x0 = threadIdx.x; x0 < total; x0 += 256 * U) {
     uint4 k[U], v[U];
@@ -767,8 +784,8 @@ __global__ void __launch_bounds__(256) append_kernel(const Cache c, int64_t Tn, 
         const int h = e / LPR;
         to[u] = s_row[t] + ((int64_t)h << shift);
         const uint4* src = uvqk + (t0 + t) * 4 * width + e;
-        v[u] = __ldcs(src + width);
-        k[u] = __ldcs(src + 3 * width);
+        v[u] = __ldg(src + width);
+        k[u] = __ldg(src + 3 * width);
         if (e % LPR == 0 && c.weights) c.weights[to[u]] = 0.0f;
         to[u] = to[u] * LPR + e % LPR;
       }
@@ -776,8 +793,8 @@ __global__ void __launch_bounds__(256) append_kernel(const Cache c, int64_t Tn, 
 #pragma unroll
     for (int u = 0; u < U; u++) {
       if (to[u] < 0) continue;
-      static_cast<uint4*>(c.k)[to[u]] = k[u];
-      static_cast<uint4*>(c.v)[to[u]] = v[u];
+      __stcs(static_cast<uint4*>(c.k) + to[u], k[u]);
+      __stcs(static_cast<uint4*>(c.v) + to[u], v[u]);
     }
   }
 }
@@ -817,9 +834,9 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
 // Selection, one cluster of CTAs per sequence, each on a contiguous part of its slots, each warp on a
 // contiguous part of that.  Every thread scores its slots; the first SEL_KEYS keys stay in registers,
 // any further ones go through the workspace.  The budget-th largest key is found by histograms of the
-// top 11, the next 11 and the last 10 bits: every CTA counts its own keys and adds its occupied bins
-// to the first CTA's, which finds the bin and tells the others; once few keys share the bits found
-// so far, the first CTA gets those keys and finishes alone.  Then every CTA lists the gaps below slot
+// top 11, the next 11 and the last 10 bits: every CTA counts its own keys, the first one sums the
+// bins through distributed shared memory, finds the bin and tells the others; once few keys share
+// the bits found so far, the first CTA gets those keys and finishes alone.  Then every CTA lists the gaps below slot
 // `budget` and the kept slots from there on among its own, in ascending order.  Eleven bits (two of
 // the mantissa) spread accumulated weights over enough bins that the shared-memory atomics seldom
 // meet; warps whose keys all fall into one bin add them at once.  Bound by latency, some ten
@@ -863,8 +880,6 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   if (tid == 0) s_listed = 0;
   for (int i = tid; i < 3 * SEL_BINS / 4; i += SEL_THREADS)
     reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
-  if (S > 1) cluster.barrier_arrive(); else __syncthreads();
-
   // scores: the loads of SEL_KEYS slots and four heads are in flight at once
   // (unconditional, from some slot where there is none: a load under a condition is waited for at once)
   uint32_t key[SEL_KEYS], page[SEL_KEYS];
@@ -935,7 +950,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
         if (r0 + i < rounds) f(start + (r0 + i) * 32, k[i], pg[i], start + (r0 + i) * 32 < n);
     }
   };
-  if (S > 1) cluster.barrier_wait();   // bins are zero everywhere
+  __syncthreads();   // bins are zero
 
   uint32_t prefix = 0, mask = 0;
   int want = budget;          // of the keys that share the prefix, how many are kept
@@ -952,19 +967,21 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       atomicAdd(&hist[bin], 1);
     }
   };
-  // the highest bin at which the count from the top reaches `want`, for all CTAs of `tell_to`
-  auto find = [&](const int* hist, int tell_to) {
+  // the highest bin at which the count from the top, over `ctas` CTAs, reaches `want`, told to them
+  auto find = [&](int* hist, int ctas) {
     constexpr int PER = SEL_BINS / SEL_THREADS;
-    int c[PER], own = 0;
+    static_assert(PER == 4, "a thread has four bins");
+    int c[PER] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < PER; i += 4) {
-      const int4 x = *reinterpret_cast<const int4*>(hist + tid * PER + i);
-      c[i] = x.x;
-      c[i + 1] = x.y;
-      c[i + 2] = x.z;
-      c[i + 3] = x.w;
-      own += x.x + x.y + x.z + x.w;
-    }
+    for (int r = 0; r < SEL_CLUSTER; r++)
+      if (r < ctas) {
+        const int4 x = reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r))[tid];
+        c[0] += x.x;
+        c[1] += x.y;
+        c[2] += x.z;
+        c[3] += x.w;
+      }
+    const int own = c[0] + c[1] + c[2] + c[3];
     int top = own;            // keys in the thread's bins and those above
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -983,7 +1000,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
           at = c[i - 1];
           d = i - 1;
         }
-      for (int r = 0; r < tell_to; r++) {
+      for (int r = 0; r < ctas; r++) {
         int* to = cluster.map_shared_rank(s_found, r);
         to[0] = tid * PER + d;
         to[1] = want - above;
@@ -1008,19 +1025,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       break;
     }
     each([&](int, uint32_t k, uint32_t, bool in) { count(hist, k, in && (k & mask) == prefix, sh, low); });
-    __syncthreads();
-    if (S > 1) {
-      int* to = cluster.map_shared_rank(hist, 0);
-      if (rank > 0)
-        for (int i = tid * 4; i < SEL_BINS; i += SEL_THREADS * 4) {
-          const int4 x = *reinterpret_cast<const int4*>(hist + i);
-          if (x.x) atomicAdd(to + i, x.x);
-          if (x.y) atomicAdd(to + i + 1, x.y);
-          if (x.z) atomicAdd(to + i + 2, x.z);
-          if (x.w) atomicAdd(to + i + 3, x.w);
-        }
-      cluster.sync();
-    }
+    sync();
     if (rank == 0) find(hist, S);
     sync();
     take(sh, low);
@@ -1194,8 +1199,8 @@ __global__ void __launch_bounds__(256, 4) evict_move_kernel(const Evict a, int c
 #pragma unroll
     for (int u = 0; u < U; u++)
       if (to[u] != ~0u) {
-        k[(int64_t)to[u] * LPR] = kr[u];
-        v[(int64_t)to[u] * LPR] = vr[u];
+        __stcs(k + (int64_t)to[u] * LPR, kr[u]);
+        __stcs(v + (int64_t)to[u] * LPR, vr[u]);
       }
   }
 }
@@ -1265,9 +1270,13 @@ inline hstu_status_t launch_append(const Cache& c, int row_bytes, int64_t T, int
                                    const void* uvqk, const int64_t* off, const int64_t* ts,
                                    const int32_t* table, int64_t max_pages, const int64_t* lens,
                                    const int64_t* next_pos, cudaStream_t st) {
-  const unsigned grid = (unsigned)((T + APPEND_TOKENS - 1) / APPEND_TOKENS);
+  // about APPEND_PIECES pieces of K a CTA: wide rows in small groups, so that the SMs get even shares
+  int tokens = APPEND_PIECES / (c.H * (row_bytes / 16));
+  tokens = tokens < 1 ? 1 : tokens > APPEND_TOKENS ? APPEND_TOKENS : tokens;
+  if ((T + tokens - 1) / tokens >= (1LL << 31)) return HSTU_ERR_UNSUPPORTED;
+  const unsigned grid = (unsigned)((T + tokens - 1) / tokens);
   auto kern = row_bytes == 128 ? append_kernel<8> : row_bytes == 256 ? append_kernel<16> : append_kernel<32>;
-  kern<<<grid, 256, 0, st>>>(c, T, B, static_cast<const uint4*>(uvqk), off, ts, table, max_pages, lens,
+  kern<<<grid, 256, 0, st>>>(c, tokens, T, B, static_cast<const uint4*>(uvqk), off, ts, table, max_pages, lens,
                              next_pos);
   return launched();
 }
