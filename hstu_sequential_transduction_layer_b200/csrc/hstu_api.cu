@@ -360,8 +360,9 @@ hstu_status_t check_cache(const hstu_paged_cache_t* c) {
   if (4LL * c->num_heads * c->head_dim > (1LL << 30)) return HSTU_ERR_INVALID_ARG;
   // rows of K, V and weights are numbered in 32 bits (2^32 rows of K alone are 512 GB and more)
   if (c->num_pages * c->page_size >= (1LL << 32) / c->num_heads) return HSTU_ERR_UNSUPPORTED;
-  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) || !aligned16(c->positions) ||
-      !aligned16(c->timestamps) || !aligned16(c->weights))
+  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return HSTU_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(c->positions) & 3) || (reinterpret_cast<uintptr_t>(c->weights) & 3) ||
+      (reinterpret_cast<uintptr_t>(c->timestamps) & 7))
     return HSTU_ERR_INVALID_ARG;
   return HSTU_OK;
 }

@@ -762,7 +762,9 @@ __global__ void __launch_bounds__(256) append_kernel(const Cache c, int tokens, 
         if (pg >= 0) {
           const int64_t o = slot & (ps - 1), at = (pg << shift) + o;
           row = ((pg * H) << shift) + o;
-          if (c.positions) c.positions[at] = (int32_t)((next_pos ? next_pos[lo] : n) + i);
+          const int64_t p = (next_pos ? next_pos[lo] : n) + i;
+          if (p < 0 || p > 0x7fffffff) report(HSTU_ERR_DEVICE_BAD_OFFSETS);
+          if (c.positions) c.positions[at] = (int32_t)(p < 0 ? 0 : p > 0x7fffffff ? 0x7fffffff : p);
           if (c.timestamps && ts) c.timestamps[at] = ts[t];
         }
       }

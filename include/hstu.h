@@ -356,7 +356,7 @@ hstu_status_t hstu_candidate_layer_fwd(const hstu_shape_t* shape, const void* uv
  * table entries beyond its own tokens are not read.  A negative cache_lens[b] marks an inactive
  * row of a padded batch.
  *
- *  num_pages     pages in the pool, below 2^31
+ *  num_pages     pages in the pool, below 2^31 (num_pages * page_size * num_heads below 2^32)
  *  page_size     tokens a page: a power of two, 16 .. 1024
  *  num_heads, head_dim (= d_qk = d_v), dtype   as the layer's; bf16: head_dim 64 or 128, fp32: 32,
  *                64 or 128 (else HSTU_ERR_UNSUPPORTED)
@@ -366,14 +366,16 @@ hstu_status_t hstu_candidate_layer_fwd(const hstu_shape_t* shape, const void* uv
  *  timestamps    [num_pages, page_size] int64 seconds, or NULL (no time table)
  *  weights       [num_pages, num_heads, page_size] fp32: sums of |a| that the token received from
  *                the tokens after it, a head; or NULL (not kept; such a cache cannot evict)
- * The caller owns every array; the struct is read during the call only.
+ * The caller owns every array (naturally aligned); the struct is read during the call only.  A
+ * page-table row names fewer than 2^30 slots (max_pages * page_size).
  *
- * Two sequences of one call may share a page that neither call writes: a shared prefix can be read
- * by hstu_paged_attention_fwd on a cache without weights; pages that are appended to, evicted from
- * or whose weights are summed belong to one sequence.  Problems only the device sees (a length
- * beyond the table or max_seq_len, an entry that is no page) are reported as
- * HSTU_ERR_DEVICE_BAD_OFFSETS: the length is clamped and the tokens of such a page are left out.
- * Calls that write one cache are ordered by the caller (one stream, or events).
+ * Sequences of one call may share pages that the call only reads: a common prefix, for
+ * hstu_paged_attention_fwd on a cache without weights.  A page that is appended to, evicted from or
+ * whose weights are summed belongs to one sequence, once.  Problems only the device sees are
+ * reported as HSTU_ERR_DEVICE_BAD_OFFSETS: a length beyond the table or max_seq_len is clamped (its
+ * new token is not stored), the tokens of an entry that is no page are left out, a position outside
+ * 0 .. 2^31 - 1 is clamped.  Calls that write one cache are ordered by the caller (one stream, or
+ * events).
  */
 typedef struct {
   int64_t num_pages;

@@ -100,7 +100,8 @@ def evict(cache, table, lens, next_positions, budget, recent):
             bad = math.isnan(total)
             rank.append((first, 1 if bad and first else 0, 0.0 if bad or not first else -total, j))
         kept = sorted(r[3] for r in sorted(rank)[:budget])
-        gaps = [j for j in range(budget) if j not in set(kept)]
+        stay = set(kept)
+        gaps = [j for j in range(budget) if j not in stay]
         for to, frm in zip(gaps, [j for j in kept if j >= budget]):
             (pt, ot), (pf, of) = _place(cache, table, b, to), _place(cache, table, b, frm)
             for name in ("k", "v", "weights"):

@@ -33,7 +33,8 @@ def shape_of(hstu, **kw):
 
 BAD_CACHES = [dict(num_pages=0), dict(num_pages=1 << 31), dict(page_size=24), dict(page_size=8),
               dict(page_size=2048), dict(page_size=0), dict(num_heads=0), dict(head_dim=0),
-              dict(dtype=5), dict(k=None), dict(v=None), dict(k=P(1) + 8), dict(v=P(2) + 2)]
+              dict(dtype=5), dict(k=None), dict(v=None), dict(k=P(1) + 8), dict(v=P(2) + 2),
+              dict(positions=P(3) + 2), dict(timestamps=P(4) + 4), dict(weights=P(5) + 1)]
 
 
 def append(hstu, cache=None, T=10, B=3, M=4, **kw):
@@ -94,6 +95,7 @@ def test_append_refusals(hstu):
     assert append(hstu, uvqk=P(6) + 2) == E
     assert append(hstu, uvqk=P(1) + 4096) == E            # reads the cache's own K
     assert append(hstu, M=0) == E and append(hstu, M=-3) == E
+    assert append(hstu, M=1 << 24) == hstu.HSTU_ERR_UNSUPPORTED          # 2^30 slots a row
     assert append(hstu, T=0) == hstu.HSTU_OK              # nothing to do
     assert append(hstu, T=0, B=0, table=None, lens=None) == hstu.HSTU_OK
 
@@ -123,6 +125,11 @@ def test_attention_refusals(hstu):
     assert attend(hstu, uvqk=P(1) + 1024) == E
     assert attend(hstu, ws=P(5)) == E
     assert attend(hstu, M=0) == E
+    assert attend(hstu, M=1 << 24) == U
+    assert attend(hstu, shape=shape_of(hstu, max_seq_len=1 << 31)) == U
+    assert attend(hstu, shape=shape_of(hstu, num_seqs=1 << 20, total_tokens=1 << 20, max_seq_len=1 << 20)) == U
+    assert attend(hstu, cache=cache_of(hstu, num_pages=(1 << 31) - 1)) == U   # rows beyond 32 bits
+    assert attend(hstu, ws_bytes=hstu.paged_attention_workspace_size(shape_of(hstu)) - 1) == E
     empty = shape_of(hstu, num_seqs=0, total_tokens=0)
     assert attend(hstu, shape=empty, uvqk=None, av=None, ws=None, table=None, lens=None) == hstu.HSTU_OK
 

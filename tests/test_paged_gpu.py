@@ -134,7 +134,7 @@ def test_attention_infinite_and_nan_keys_stay_in_their_sequence(hstu):
     assert (torch.isfinite(got).cpu().numpy() == fine).all() and not fine[0, 0].any()
     assert fine[0, 1].all() and fine[1].all()
     ab = c.bounds()[0].reshape(2, 2, 64)
-    assert (np.abs(got.double().cpu().numpy() - av)[fine] <= ab[fine]).all()
+    assert (np.abs(got.double().cpu().numpy()[fine] - av[fine]) <= ab[fine]).all()
 
 
 def test_attention_bad_lengths_and_pages_are_reported(hstu):
@@ -193,31 +193,83 @@ def test_attention_far_into_a_large_pool(hstu):
 
 
 def test_attention_captured_and_replayed(hstu):
-    c = Case(23, [700, 20, 0], 4, 64, 16)
-    g = c.on_device(hstu)
-    ws = torch.empty(max(256, hstu.paged_attention_workspace_size(g["shape"])), dtype=torch.uint8,
+    # two graphs share one workspace; each step's graph advances the lengths itself
+    c = Case(23, [700, 20, 0], 4, 64, 16, extra=12)
+    ws = torch.empty(hstu.paged_attention_workspace_size(c.on_device(hstu)["shape"]), dtype=torch.uint8,
                      device="cuda")
-    eager = c.on_device(hstu)
+    gs = [c.on_device(hstu) for _ in range(3)]
+    for g in gs:
+        s = g["shape"]
+        g["shape"] = hstu.make_shape(3, 3, 712, s.d_model, 4, 64, 64, hstu.HSTU_BF16,
+                                     s.n_pos_buckets, s.n_time_buckets)
+    graphs = []
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.stream(st):
+    for g in gs[:2]:
+        graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=st):
             c.attend(hstu, g, workspace=ws)
             g["lens"].add_(1)
             g["next"].add_(1)
+        graphs.append(graph)
     torch.cuda.synchronize()
     ws.fill_(255)                                            # whatever it held before
-    for step in range(5):
-        graph.replay()
+    eager = gs[2]
+    for step in range(8):
+        for graph in graphs:
+            graph.replay()
         c.attend(hstu, eager)
         eager["lens"].add_(1)
         eager["next"].add_(1)
         torch.cuda.synchronize()
-        # max_seq_len is one token more than the first step's longest: the later steps clamp
-        if step == 0:
-            assert torch.equal(g["av"], eager["av"])
-    hstu.device_status()
+        for g in gs[:2]:
+            assert torch.equal(g["av"], eager["av"]), step
+            assert torch.equal(g["cache"].k.isnan(), eager["cache"].k.isnan())
+    assert hstu.device_status() == hstu.HSTU_OK
+
+
+@pytest.mark.parametrize("lens", [[(i * 7) % 23 - 1 for i in range(900)], [i % 4 - 1 for i in range(5000)],
+                                  [0] * 385, [200] + [-1] * 800 + [333], [-1] * 700 + [17]])
+def test_attention_more_sequences_than_threads(hstu, lens):
+    # lengths are scanned in groups of more than one; empty groups and groups of inactive ones
+    attention_case(hstu, Case(25, lens, 1, 64, 16, "fp32", bias="pos"))
+
+
+def test_attention_wide_models(hstu):
+    attention_case(hstu, Case(26, [61, 18, 130], 33, 128, 32))
+    attention_case(hstu, Case(27, [70, 9], 48, 32, 16, "fp32", bias="alibi"))
+
+
+def test_attention_lengths_beyond_the_announced_longest_are_clamped(hstu):
+    c = Case(28, [100, 40], 2, 64, 16, extra=30)
+    g = c.on_device(hstu)
+    s = g["shape"]
+    g["shape"] = hstu.make_shape(2, 2, 81, s.d_model, 2, 64, 64, hstu.HSTU_BF16, s.n_pos_buckets,
+                                 s.n_time_buckets)
+    k = g["cache"].k.clone()
+    c.attend(hstu, g)
+    assert hstu.device_status() == hstu.HSTU_ERR_DEVICE_BAD_OFFSETS
+    c.lens[0] = 80                       # and its new token is not stored
+    av, _ = c.want_attention(append=False)
+    check_av(g["av"], av, c.bounds()[0])
+    p = int(c.table[0, 80 // 16])
+    assert torch.equal(g["cache"].k[p], k[p])
+    same(g["cache"].k[c.table[1, 40 // 16]][:, 40 % 16], c.uvqk.reshape(2, 4, 2, 64)[1, 3], "stored row")
+
+
+def test_positions_outside_their_range_are_reported(hstu):
+    for bad in (1 << 31, -1, 1 << 40):
+        c = Case(29, [20], 1, 64, 16, bias="pos")
+        g = c.on_device(hstu)
+        g["next"][0] = bad
+        c.attend(hstu, g)
+        assert hstu.device_status() == hstu.HSTU_ERR_DEVICE_BAD_OFFSETS
+        assert torch.isfinite(g["av"]).all()
+        off = torch.tensor([0, 3], device="cuda")
+        g["lens"][0] = 3
+        hstu.hstu_cache_append(g["cache"], c.dev(values(c.rng, (3, 256), "bf16"), torch.bfloat16), off,
+                               None, g["table"], g["lens"], g["next"])
+        assert hstu.device_status() == hstu.HSTU_ERR_DEVICE_BAD_OFFSETS
 
 
 def test_attention_on_two_streams_at_once(hstu):
@@ -244,6 +296,8 @@ def test_attention_on_two_streams_at_once(hstu):
     ("fp32", 2, 32, 16, [7, 0], [9, 33]),
     ("fp32", 1, 128, 32, [1], [31]),
     ("bf16", 8, 64, 64, [0, 0, 0, 1], [0, 0, 700, 0]),
+    ("fp32", 65, 128, 16, [3, 0], [20, 1]),
+    ("bf16", 2, 128, 256, [0], [1]),
     ("bf16", 1, 64, 16, [0] * 300, [i % 7 for i in range(300)])])
 def test_append(hstu, dtype, H, hd, ps, lens, counts):
     c = Case(31, lens, H, hd, ps, dtype, thinned=True, extra=max(counts))
@@ -331,8 +385,27 @@ def test_evict_a_long_history(hstu):
     evict_case(hstu, Case(44, [20011, 5], 1, 64, 64, bias="none"), 7001, 500)
 
 
-def test_evict_many_sequences(hstu):
-    evict_case(hstu, Case(45, [i % 50 for i in range(400)], 1, 64, 16, bias="none"), 20, 4)
+@pytest.mark.parametrize("kind", ["random", "zero", "two values"])
+def test_evict_histories_beyond_the_registers(hstu, kind):
+    # more slots than a cluster of eight CTAs keeps in registers: keys go through the workspace
+    c = Case(48, [70001, 100], 1, 64, 1024, bias="none")
+    live = ~np.isnan(c.cache["weights"])
+    if kind != "random":
+        c.cache["weights"][live] = 0.0 if kind == "zero" else c.rng.integers(0, 2, live.sum())
+    evict_case(hstu, c, 30011, 1000)
+
+
+@pytest.mark.parametrize("n", [400, 3000])
+def test_evict_many_sequences(hstu, n):
+    evict_case(hstu, Case(45, [i % 50 for i in range(n)], 1, 64, 16, bias="none"), 20, 4)
+
+
+def test_evict_close_weights(hstu):
+    # keys that differ in the last bits only: every pass of the search is needed
+    c = Case(49, [4000, 900], 1, 64, 64, bias="none")
+    live = ~np.isnan(c.cache["weights"])
+    c.cache["weights"][live] = (np.float32(1.0) + c.rng.integers(0, 1500, live.sum()) * np.float32(2.0 ** -23))
+    evict_case(hstu, c, 801, 16)
 
 
 def test_evict_captured_with_a_dirty_workspace(hstu):
@@ -431,6 +504,40 @@ def test_layer_inactive_rows_do_not_disturb_the_batch(hstu):
         out.append(cache.k)
     assert torch.equal(out[0][[0, 2]], out[2][[0, 2]]) and torch.isfinite(out[2].float()).all()
     assert torch.equal(out[1][[0, 2]], out[3][[0, 2]]) and (out[3][1] == 0).all()
+
+
+def test_layer_captured_equals_eager(hstu):
+    inp = history_case(53, [1, 1], 2, 64, "bf16")
+    p = inp.layers[0]
+    W = [dev(getattr(p, k)) for k in ("W1", "b1", "W2", "b2", "ln_w", "ln_b")]
+    tab = [dev(inp.pos_table, "f32"), dev(inp.time_table, "f32"), None]
+    s = hstu.make_shape(2, 2, 30, 128, 2, 64, 64, hstu.HSTU_BF16, 64, 16)
+    table = torch.arange(4, dtype=torch.int32, device="cuda").reshape(2, 2)
+    now = torch.from_numpy(np.ascontiguousarray(inp.timestamps)).cuda()
+    runs = []
+    for captured in (False, True):
+        cache, X = hstu.PagedCache.allocate(4, 16, 2, 64), dev(inp.X)
+        lens = torch.tensor([0, 0], device="cuda")
+        ws = torch.empty(hstu.paged_layer_workspace_size(s), dtype=torch.uint8, device="cuda")
+
+        def step():   # the output is the next step's input
+            y = hstu.hstu_paged_layer_fwd(s, cache, X, table, lens, None, now, *W, *tab, inp.scale,
+                                          workspace=ws)
+            X.copy_(y)
+            lens.add_(1)
+        if captured:
+            graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+            with torch.cuda.graph(graph, stream=st):
+                step()
+            for _ in range(20):
+                graph.replay()
+        else:
+            for _ in range(20):
+                step()
+        torch.cuda.synchronize()
+        runs.append((X.clone(), cache.k.clone(), cache.weights.clone(), lens.clone()))
+    assert hstu.device_status() == hstu.HSTU_OK
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
 
 
 @pytest.mark.parametrize("dtype,H,hd,bias", [("bf16", 4, 64, "rab"), ("fp32", 2, 32, "alibi")])
