@@ -82,6 +82,13 @@ __device__ __forceinline__ int64_t div_by(int64_t a, int b) {
   return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
+// Programmatic dependent launch: a kernel may be launched while the one before it in the stream
+// finishes, and touches global memory only after `after_previous`; `let_next` allows the same to
+// the next one.  (Every kernel of this file is launched so: without it a launch costs a microsecond
+// or two between kernels that take a few.)
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // 16 bytes of T as pairs of fp32.
 template <typename T> struct vec16;
 template <> struct vec16<float> {
@@ -238,10 +245,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
     }
     sm100::fence_mbar_init();
   }
-  if (threadIdx.x == 0) {
-    s_abort = 0;
-    recs[blockIdx.x] = {-1, 0};
-  }
+  if (threadIdx.x == 0) s_abort = 0;
+  after_previous();
+  if (threadIdx.x == 0) recs[blockIdx.x] = {-1, 0};
   // tiles a head up to each group of C sequences; with C = 1 the lengths stay in shared memory
   const int C = (B + ATTN_THREADS - 1) / ATTN_THREADS;
   {
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attention_kernel(const Attn a
       if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort))) break;
       __nanosleep(ATTN_NAP);
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next();
   } else {
     const int gw = blockIdx.x * ATTN_WARPS + warp;
     const int count = (int)(share + ((uint32_t)gw < over ? 1 : 0));
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(ATTN_MAX_CTAS) attention_join_kernel(float* av
   constexpr int L = HD / 4, G = ATTN_MAX_CTAS / L;   // lanes a row, rows at a time
   __shared__ int s_end, s_flag[ATTN_MAX_CTAS];
   __shared__ float4 red[G][L];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   const int c = blockIdx.x, pair = recs[c].pair;
   if (threadIdx.x == 0) s_end = ctas - 1;
   const int flag = threadIdx.x < ctas ? recs[threadIdx.x].before : 0;
@@ -737,6 +743,7 @@ __global__ void __launch_bounds__(256) append_kernel(const Cache c, int tokens, 
                                                      const int64_t* __restrict__ lens,
                                                      const int64_t* __restrict__ next_pos) {
   __shared__ int64_t s_row[APPEND_TOKENS];   // the token's row of head 0, or -1
+  after_previous();
   // the offsets' own check, over all CTAs
   for (int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x; s <= B; s += (int64_t)gridDim.x * 256) {
     const int64_t v = off[s];
@@ -858,7 +865,11 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   __shared__ int s_found[3];                   // the bin that holds the key searched, how many of its
                                                // keys are kept, and how many there are
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) s_listed = 0;
+  for (int i = tid; i < 3 * SEL_BINS / 4; i += SEL_THREADS)
+    reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
+  after_previous();
+  let_next();
   const int64_t b = blockIdx.x / S, len = a.lens[b], n64 = cached_len(len, a.room);
   if (n64 <= a.budget) {
     if (rank == 0 && tid == 0) {
@@ -879,9 +890,6 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   const int64_t oldest = (a.next_pos ? a.next_pos[b] : n64) - a.recent;
   uint32_t* spill = a.keys + b * a.room;
 
-  if (tid == 0) s_listed = 0;
-  for (int i = tid; i < 3 * SEL_BINS / 4; i += SEL_THREADS)
-    reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
   // scores: the loads of SEL_KEYS slots and four heads are in flight at once
   // (unconditional, from some slot where there is none: a load under a condition is waited for at once)
   uint32_t key[SEL_KEYS], page[SEL_KEYS];
@@ -1156,7 +1164,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
 template <int LPR>
 __global__ void __launch_bounds__(256, 4) evict_move_kernel(const Evict a, int ctas) {
   constexpr int R = 256 / LPR, U = 4;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   const int64_t b = blockIdx.x / ctas;
   const int part = (int)(blockIdx.x % ctas), H = a.c.H, shift = a.c.ps_shift, ps = 1 << shift;
   const int sub = threadIdx.x % LPR;
@@ -1211,9 +1219,26 @@ __global__ void __launch_bounds__(256, 4) evict_move_kernel(const Evict a, int c
 // Launchers (arguments already checked)
 // ------------------------------------------------------------------------------------------------
 
-inline hstu_status_t launched() {
+// Launches a kernel of this file (see after_previous), `cluster` CTAs a cluster.
+template <typename... P, typename... A>
+hstu_status_t launch(void (*kern)(P...), int64_t grid, int threads, int smem, int cluster, cudaStream_t st,
+                     A... args) {
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  const bool ok = cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess;
   count_launch();
-  return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  return ok && cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
 inline bool head_dim_supported(int dtype, int hd) {
@@ -1239,23 +1264,10 @@ hstu_status_t launch_attention_t(const Attn& a, void* ws, int sms, cudaStream_t 
   auto kern = attention_kernel<T, HD>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
     return HSTU_ERR_CUDA;
-  kern<<<(unsigned)grid, ATTN_THREADS, SMEM, st>>>(a, parts, recs);
-  hstu_status_t rc = launched();
+  const hstu_status_t rc = launch(kern, grid, ATTN_THREADS, SMEM, 0, st, a, parts, recs);
   // one CTA joins its warps' parts itself, and a single tile a (sequence, head) has no parts
   if (rc != HSTU_OK || grid == 1 || a.max_len < TILE) return rc;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its launch overlaps the attention
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(ATTN_MAX_CTAS);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attention_join_kernel<HD>, a.av, (const float*)parts,
-                         (const Part*)recs, (int)grid) != cudaSuccess)
-    return HSTU_ERR_CUDA;
-  return launched();
+  return launch(attention_join_kernel<HD>, grid, ATTN_MAX_CTAS, 0, 0, st, a.av, parts, recs, (int)grid);
 }
 
 inline hstu_status_t launch_attention(const Attn& a, int dtype, int hd, void* ws, int sms,
@@ -1276,41 +1288,22 @@ inline hstu_status_t launch_append(const Cache& c, int row_bytes, int64_t T, int
   int tokens = APPEND_PIECES / (c.H * (row_bytes / 16));
   tokens = tokens < 1 ? 1 : tokens > APPEND_TOKENS ? APPEND_TOKENS : tokens;
   if ((T + tokens - 1) / tokens >= (1LL << 31)) return HSTU_ERR_UNSUPPORTED;
-  const unsigned grid = (unsigned)((T + tokens - 1) / tokens);
   auto kern = row_bytes == 128 ? append_kernel<8> : row_bytes == 256 ? append_kernel<16> : append_kernel<32>;
-  kern<<<grid, 256, 0, st>>>(c, tokens, T, B, static_cast<const uint4*>(uvqk), off, ts, table, max_pages, lens,
-                             next_pos);
-  return launched();
+  return launch(kern, (T + tokens - 1) / tokens, 256, 0, 0, st, c, tokens, T, B,
+                static_cast<const uint4*>(uvqk), off, ts, table, max_pages, lens, next_pos);
 }
 
 inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaStream_t st) {
-  cudaLaunchAttribute attr[1]{};
-  cudaLaunchConfig_t cfg{};
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   // as many CTAs as hold the keys of a row's slots in registers, and more while there are SMs for
   // them, at most 8
   int S = 1;
   while (S < SEL_CLUSTER && ((int64_t)S * SEL_THREADS * SEL_KEYS < a.room || 2 * S * a.B <= sms)) S *= 2;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(a.B * S));
-  cfg.blockDim = dim3(SEL_THREADS);
-  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess) return HSTU_ERR_CUDA;
-  hstu_status_t rc = launched();
+  const hstu_status_t rc = launch(evict_select_kernel, a.B * S, SEL_THREADS, 0, S, st, a);
   if (rc != HSTU_OK) return rc;
   // twice what fits the SMs at once, over all sequences; at least one each
-  int64_t ctas = (8LL * sms + a.B - 1) / a.B;
-  attr[0] = cudaLaunchAttribute{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its launch overlaps the selection
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(a.B * ctas));
-  cfg.blockDim = dim3(256);
+  const int64_t ctas = (8LL * sms + a.B - 1) / a.B;
   auto kern = row_bytes == 128 ? evict_move_kernel<8> : row_bytes == 256 ? evict_move_kernel<16> : evict_move_kernel<32>;
-  if (cudaLaunchKernelEx(&cfg, kern, a, (int)ctas) != cudaSuccess) return HSTU_ERR_CUDA;
-  return launched();
+  return launch(kern, a.B * ctas, 256, 0, 0, st, a, (int)ctas);
 }
 
 }  // namespace paged
