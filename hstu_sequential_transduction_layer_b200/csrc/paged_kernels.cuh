@@ -843,9 +843,10 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
 // Selection, one cluster of CTAs per sequence, each on a contiguous part of its slots, each warp on a
 // contiguous part of that.  Every thread scores its slots; the first SEL_KEYS keys stay in registers,
 // any further ones go through the workspace.  The budget-th largest key is found by histograms of the
-// top 11, the next 11 and the last 10 bits: every CTA counts its own keys, the first one sums the
-// bins through distributed shared memory, finds the bin and tells the others; once few keys share
-// the bits found so far, the first CTA gets those keys and finishes alone.  Then every CTA lists the gaps below slot
+// top 11, the next 11 and the last 10 bits: every CTA counts its own keys, sums all CTAs' bins
+// through distributed shared memory and finds the bin for itself; once few keys share the bits found
+// so far, every CTA gathers those and finishes alone, with one cluster barrier a step (about a
+// thousand clocks each).  Then every CTA lists the gaps below slot
 // `budget` and the kept slots from there on among its own, in ascending order.  Eleven bits (two of
 // the mantissa) spread accumulated weights over enough bins that the shared-memory atomics seldom
 // meet; warps whose keys all fall into one bin add them at once.  Bound by latency, some ten
@@ -858,8 +859,8 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   __shared__ __align__(16) int s_hist[3][SEL_BINS];
-  __shared__ uint32_t s_list[SEL_LIST];
-  __shared__ int s_listed;
+  __shared__ uint32_t s_list[SEL_LIST], s_gathered[SEL_LIST];
+  __shared__ int s_listed, s_groups[3][SEL_CLUSTER][SEL_BINS / 32];
   __shared__ int s_warp[SEL_WARPS], s_gaps[SEL_WARPS], s_movers[SEL_WARPS];
   __shared__ int s_count[3][SEL_CLUSTER];      // equal keys, gaps and movers of the cluster's CTAs
   __shared__ int s_found[3];                   // the bin that holds the key searched, how many of its
@@ -977,46 +978,52 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       atomicAdd(&hist[bin], 1);
     }
   };
-  // the highest bin at which the count from the top, over `ctas` CTAs, reaches `want`, told to them
-  auto find = [&](int* hist, int ctas) {
-    constexpr int PER = SEL_BINS / SEL_THREADS;
-    static_assert(PER == 4, "a thread has four bins");
-    int c[PER] = {0, 0, 0, 0};
-#pragma unroll
-    for (int r = 0; r < SEL_CLUSTER; r++)
-      if (r < ctas) {
-        const int4 x = reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r))[tid];
-        c[0] += x.x;
-        c[1] += x.y;
-        c[2] += x.z;
-        c[3] += x.w;
-      }
-    const int own = c[0] + c[1] + c[2] + c[3];
-    int top = own;            // keys in the thread's bins and those above
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_down_sync(0xffffffffu, top, o);
-      if (lane + o < 32) top += y;
+  // The highest bin at which the count from the top reaches `want`, of the cluster's bins or of the
+  // CTA's own.  CTAs exchange the sums of groups of 32 bins; the bins of the one group that matters
+  // are then read from all of them.
+  auto find = [&](int pass, bool all) {
+    int* hist = s_hist[pass];
+    const int ctas = all ? S : 1;
+    for (int c = warp; c < SEL_BINS / 32; c += SEL_WARPS) {
+      const int sum = __reduce_add_sync(0xffffffffu, hist[c * 32 + lane]);
+      if (lane < ctas) *(all ? cluster.map_shared_rank(&s_groups[pass][rank][c], lane) : &s_groups[pass][0][c]) = sum;
     }
-    if (lane == 0) s_warp[warp] = top;
-    __syncthreads();
-    top += __reduce_add_sync(0xffffffffu, lane > warp && lane < SEL_WARPS ? s_warp[lane] : 0);
-    if (want == 0 ? tid == SEL_THREADS - 1 : top >= want && top - own < want) {
-      int above = top - own, d = PER - 1, at = c[PER - 1];
-#pragma unroll
-      for (int i = PER - 1; i > 0; i--)
-        if (d == i && above + c[i] < want) {
-          above += c[i];
-          at = c[i - 1];
-          d = i - 1;
-        }
+    if (all) sync(); else __syncthreads();
+    if (warp == 0) {
+      static_assert(SEL_BINS / 32 == 64, "a lane has two groups");
+      int lo = 0, hi = 0;     // of groups 2 * lane and 2 * lane + 1
       for (int r = 0; r < ctas; r++) {
-        int* to = cluster.map_shared_rank(s_found, r);
-        to[0] = tid * PER + d;
-        to[1] = want - above;
-        to[2] = at;
+        lo += s_groups[pass][r][2 * lane];
+        hi += s_groups[pass][r][2 * lane + 1];
+      }
+      auto from_top = [&](int x) {   // sum over this lane and those above
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_down_sync(0xffffffffu, x, o);
+          if (lane + o < 32) x += y;
+        }
+        return x;
+      };
+      auto holder = [&](int top) {   // the highest lane at which it reaches `want`
+        const unsigned m = __ballot_sync(0xffffffffu, top >= want);
+        return m ? 31 - __clz(m) : 0;
+      };
+      const int top = from_top(lo + hi), l = holder(top);
+      int above = __shfl_sync(0xffffffffu, top - lo - hi, l);
+      const int upper = __shfl_sync(0xffffffffu, hi, l);
+      const bool in_upper = above + upper >= want;
+      if (!in_upper) above += upper;
+      const int g = 2 * l + in_upper;
+      int bin = 0;
+      for (int r = 0; r < ctas; r++) bin += (all ? cluster.map_shared_rank(hist, r) : hist)[g * 32 + lane];
+      const int fine = above + from_top(bin), f = holder(fine);
+      if (lane == f) {
+        s_found[0] = g * 32 + f;
+        s_found[1] = want - (fine - bin);
+        s_found[2] = bin;
       }
     }
+    __syncthreads();
   };
   auto take = [&](int sh, uint32_t low) {
     prefix |= (uint32_t)s_found[0] << sh;
@@ -1035,53 +1042,46 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       break;
     }
     each([&](int, uint32_t k, uint32_t, bool in) { count(hist, k, in && (k & mask) == prefix, sh, low); });
-    sync();
-    if (rank == 0) find(hist, S);
-    sync();
+    __syncthreads();
+    find(pass, true);
     take(sh, low);
     sh = pass == 0 ? 10 : 0;
-    if (S == 1) __syncthreads();   // s_found is read before it is written again
+    __syncthreads();   // s_found is read before it is written again
   }
   if (listed) {
-    uint32_t* list = cluster.map_shared_rank(s_list, 0);
-    int* end = cluster.map_shared_rank(&s_listed, 0);
     each([&](int, uint32_t k, uint32_t, bool in) {
       const bool counts = in && (k & mask) == prefix;
       const unsigned m = __ballot_sync(0xffffffffu, counts);
       if (m == 0) return;
       int at = 0;
-      if (lane == __ffs(m) - 1) at = atomicAdd(end, __popc(m));
+      if (lane == __ffs(m) - 1) at = atomicAdd(&s_listed, __popc(m));
       at = __shfl_sync(0xffffffffu, at, __ffs(m) - 1) + __popc(m & ((1u << lane) - 1u));
-      if (counts) list[at] = k;
+      if (counts) s_list[at] = k;
     });
     sync();
-    if (rank == 0) {
-#pragma unroll 1
-      for (; pass < 3 && in_bin != want; pass++) {
-        const uint32_t low = pass < 2 ? 2047u : 1023u;
-        for (int j0 = warp * 32; j0 < s_listed; j0 += SEL_THREADS) {
-          const int j = j0 + lane;
-          const uint32_t k = j < s_listed ? s_list[j] : 0u;
-          count(s_hist[pass], k, j < s_listed && (k & mask) == prefix, sh, low);
-        }
-        __syncthreads();
-        find(s_hist[pass], 1);
-        __syncthreads();
-        take(sh, low);
-        sh = pass == 0 ? 10 : 0;
-        __syncthreads();
-      }
-      if (tid < S) {
-        int* to = cluster.map_shared_rank(s_found, tid);
-        to[0] = (int)prefix;
-        to[1] = want;
-        to[2] = in_bin;
-      }
+    // all CTAs' lists, in_bin keys in all
+    for (int r = 0, base = 0; r < S; r++) {
+      const int some = *cluster.map_shared_rank(&s_listed, r);
+      const uint32_t* list = cluster.map_shared_rank(s_list, r);
+      for (int i = tid; i < some; i += SEL_THREADS) s_gathered[base + i] = list[i];
+      base += some;
     }
-    sync();
-    prefix = (uint32_t)s_found[0];
-    want = s_found[1];
-    in_bin = s_found[2];
+    __syncthreads();
+    const int listed_keys = in_bin;
+#pragma unroll 1
+    for (; pass < 3 && in_bin != want; pass++) {
+      const uint32_t low = pass < 2 ? 2047u : 1023u;
+      for (int j0 = warp * 32; j0 < listed_keys; j0 += SEL_THREADS) {
+        const int j = j0 + lane;
+        const uint32_t k = j < listed_keys ? s_gathered[j] : 0u;
+        count(s_hist[pass], k, j < listed_keys && (k & mask) == prefix, sh, low);
+      }
+      __syncthreads();
+      find(pass, false);
+      take(sh, low);
+      sh = pass == 0 ? 10 : 0;
+      __syncthreads();
+    }
   }
   const bool ties = in_bin != want;   // else all of them are kept: every key >= prefix
 
