@@ -50,8 +50,7 @@ struct Attn {
 };
 
 // Page of a sequence's slot, or -1 (reported) when the table's entry is no page.
-__device__ __forceinline__ int64_t page_of(const int32_t* __restrict__ row, int64_t entry,
-                                           int64_t num_pages) {
+__device__ __forceinline__ int64_t page_of(const int32_t* row, int64_t entry, int64_t num_pages) {
   const int64_t p = row[entry];
   if (p < 0 || p >= num_pages) {
     report(HSTU_ERR_DEVICE_BAD_OFFSETS);
@@ -60,8 +59,7 @@ __device__ __forceinline__ int64_t page_of(const int32_t* __restrict__ row, int6
   return p;
 }
 
-// Cached length of sequence b, clamped to what its page-table row (and the announced longest
-// length) can hold with `extra` more tokens; -1 for an inactive sequence.
+// A sequence's cached length, clamped (and reported) to `most`; -1 for an inactive sequence.
 __device__ __forceinline__ int64_t cached_len(int64_t len, int64_t most) {
   if (len < 0) return -1;
   if (len > most) {
@@ -84,8 +82,10 @@ __device__ __forceinline__ int64_t div_by(int64_t a, int b) {
 
 // Programmatic dependent launch: a kernel may be launched while the one before it in the stream
 // finishes, and touches global memory only after `after_previous`; `let_next` allows the same to
-// the next one.  (Every kernel of this file is launched so: without it a launch costs a microsecond
-// or two between kernels that take a few.)
+// the next one.  Every kernel of this file is launched so: without it a launch costs a microsecond
+// or two between kernels that take a few (an eviction of 48 histories 34.4 us a call, with it 30.9).
+// What an earlier kernel may have written is therefore read by plain loads only: the compiler may
+// move loads that it takes for invariant (__ldg, const __restrict__) above the wait.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -128,7 +128,7 @@ constexpr int ATTN_STAGES = 2;
 constexpr int ATTN_INFOS = 4;                   // tiles told of: two in flight and two ahead
 static_assert(ATTN_STAGES == 2 && ATTN_INFOS == ATTN_STAGES + 2, "the start tells of and fills two stages");
 constexpr int ATTN_THREADS = (ATTN_WARPS + 1) * 32;
-constexpr int ATTN_NAP = 30;                   // ns between the producer's looks for work
+constexpr int ATTN_NAP = 30;                    // ns between the producer's looks for work
 constexpr int ATTN_HALF = 4096;                 // bytes of a tile's K, and of its V
 // CTAs of the attention: one a SM, at most this many (the workspace holds a part record for each).
 constexpr int ATTN_MAX_CTAS = 256;
@@ -735,13 +735,10 @@ __global__ void __launch_bounds__(ATTN_MAX_CTAS) attention_join_kernel(float* av
 constexpr int APPEND_TOKENS = 32, APPEND_PIECES = 1024;
 template <int LPR>
 __global__ void __launch_bounds__(256) append_kernel(const Cache c, int tokens, int64_t Tn, int64_t B,
-                                                     const uint4* __restrict__ uvqk,
-                                                     const int64_t* __restrict__ off,
-                                                     const int64_t* __restrict__ ts,
-                                                     const int32_t* __restrict__ table,
-                                                     int64_t max_pages,
-                                                     const int64_t* __restrict__ lens,
-                                                     const int64_t* __restrict__ next_pos) {
+                                                     const uint4* uvqk, const int64_t* off,
+                                                     const int64_t* ts, const int32_t* table,
+                                                     int64_t max_pages, const int64_t* lens,
+                                                     const int64_t* next_pos) {
   __shared__ int64_t s_row[APPEND_TOKENS];   // the token's row of head 0, or -1
   after_previous();
   // the offsets' own check, over all CTAs
@@ -793,8 +790,8 @@ __global__ void __launch_bounds__(256) append_kernel(const Cache c, int tokens, 
         const int h = e / LPR;
         to[u] = s_row[t] + ((int64_t)h << shift);
         const uint4* src = uvqk + (t0 + t) * 4 * width + e;
-        v[u] = __ldg(src + width);
-        k[u] = __ldg(src + 3 * width);
+        v[u] = src[width];
+        k[u] = src[3 * width];
         if (e % LPR == 0 && c.weights) c.weights[to[u]] = 0.0f;
         to[u] = to[u] * LPR + e % LPR;
       }
@@ -845,12 +842,15 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
 // any further ones go through the workspace.  The budget-th largest key is found by histograms of the
 // top 11, the next 11 and the last 10 bits: every CTA counts its own keys, sums all CTAs' bins
 // through distributed shared memory and finds the bin for itself; once few keys share the bits found
-// so far, every CTA gathers those and finishes alone, with one cluster barrier a step (about a
-// thousand clocks each).  Then every CTA lists the gaps below slot
-// `budget` and the kept slots from there on among its own, in ascending order.  Eleven bits (two of
-// the mantissa) spread accumulated weights over enough bins that the shared-memory atomics seldom
-// meet; warps whose keys all fall into one bin add them at once.  Bound by latency, some ten
-// dependent steps, and by the instructions of code that runs once: few warps, and several CTAs.
+// so far, every CTA gathers those and finishes alone, with one cluster barrier a step.  Then every
+// CTA lists the gaps below slot `budget` and the kept slots from there on among its own, in ascending
+// order.  Eleven bits (two of the mantissa) spread accumulated weights over enough bins that the
+// shared-memory atomics seldom meet; warps whose keys all fall into one bin add them at once.
+//
+// Bound by latency: 8 sequences of 8192 slots and 8 heads take 20 600 clocks (10.7 us): the scores
+// 7400, the search 9100 (two passes), the lists 4100.  Hence several CTAs a sequence (with one, 19 us)
+// and 512 threads (256: 5 us longer for 32 771 slots; 1024: the instructions that every warp repeats
+// weigh).  Exchanging whole histograms through distributed shared memory took 2 us longer.
 constexpr int SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32, SEL_KEYS = 8, SEL_CLUSTER = 8;
 constexpr int SEL_BINS = 2048, SEL_LIST = 1024;
 
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       for (int u = 0; u < 4; u++)
 #pragma unroll
         for (int i = 0; i < SEL_KEYS; i++)
-          w[u][i] = __ldg(a.c.weights + at[i] + ((uint32_t)(h + u < H ? h + u : H - 1) << shift));
+          w[u][i] = a.c.weights[at[i] + ((uint32_t)(h + u < H ? h + u : H - 1) << shift)];
 #pragma unroll
       for (int u = 0; u < 4; u++)
 #pragma unroll

@@ -540,6 +540,39 @@ def test_layer_captured_equals_eager(hstu):
     assert all(torch.equal(a, b) for a, b in zip(*runs))
 
 
+def test_calls_back_to_back_see_each_others_writes(hstu):
+    # every kernel's launch overlaps the one before it: unwaited steps equal steps waited for one by one
+    runs = []
+    for wait in (False, True):
+        c = Case(62, [900, 30, 2000, 500], 4, 128, 16, extra=70)
+        g = c.on_device(hstu)
+        s = g["shape"]
+        g["shape"] = hstu.make_shape(4, 4, 2071, s.d_model, 4, 128, 128, hstu.HSTU_BF16,
+                                     s.n_pos_buckets, s.n_time_buckets)
+        ws = torch.empty(hstu.paged_attention_workspace_size(g["shape"]), dtype=torch.uint8, device="cuda")
+        es = torch.empty(hstu.cache_evict_workspace_size(g["cache"], 4, c.M), dtype=torch.uint8, device="cuda")
+        out = []
+        torch.cuda.synchronize()
+        for step in range(60):
+            c.attend(hstu, g, workspace=ws)
+            out.append(g["av"].clone())
+            if wait:
+                torch.cuda.synchronize()
+            g["lens"].add_(1)
+            g["next"].add_(1)
+            g["uvqk"].copy_((out[-1][:, :1] * 1e-3).to(torch.bfloat16) + g["uvqk"].roll(7, 1))
+            if step % 20 == 19:
+                hstu.hstu_cache_evict(g["cache"], g["table"], g["lens"], g["next"], 800, 50,
+                                      new_lens=g["lens"], workspace=es)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert hstu.device_status() == hstu.HSTU_OK
+        runs.append((torch.stack(out), g["cache"].k, g["cache"].weights, g["cache"].positions, g["lens"]))
+    for a, b in zip(*runs):
+        assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
 @pytest.mark.parametrize("dtype,H,hd,bias", [("bf16", 4, 64, "rab"), ("fp32", 2, 32, "alibi")])
 def test_serving_loop(hstu, dtype, H, hd, bias):
     """Fill, then token after token with an eviction whenever a sequence outgrows its budget, against
