@@ -849,9 +849,8 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
 //
 // Bound by latency: 8 sequences of 8192 slots and 8 heads take 20 600 clocks (10.7 us): the scores
 // 7400, the search 9100 (two passes), the lists 4100.  Hence several CTAs a sequence (with one, 19 us)
-// and 512 threads (256: 5 us longer for 32 771 slots; 1024: the instructions that every warp repeats
-// weigh).  Exchanging whole histograms through distributed shared memory took 2 us longer.
-constexpr int SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32, SEL_KEYS = 8, SEL_CLUSTER = 8;
+// and 512 threads (256: 5 us longer for 32 771 slots).  Exchanging whole histograms through distributed shared memory took 2 us longer.
+constexpr int SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32, SEL_KEYS = 8, SEL_CLUSTER = 16;
 constexpr int SEL_BINS = 2048, SEL_LIST = 1024;
 
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a) {
@@ -1237,8 +1236,9 @@ hstu_status_t launch(void (*kern)(P...), int64_t grid, int threads, int smem, in
   cfg.attrs = attr;
   cfg.numAttrs = cluster ? 2 : 1;
   const bool ok = cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess;
+  if (cudaGetLastError() != cudaSuccess || !ok) return HSTU_ERR_CUDA;
   count_launch();
-  return ok && cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  return HSTU_OK;
 }
 
 inline bool head_dim_supported(int dtype, int hd) {
@@ -1294,11 +1294,18 @@ inline hstu_status_t launch_append(const Cache& c, int row_bytes, int64_t T, int
 }
 
 inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaStream_t st) {
-  // as many CTAs as hold the keys of a row's slots in registers, and more while there are SMs for
-  // them, at most 8
+  // As many CTAs as hold the keys of a row's slots in registers, and more while there are SMs for
+  // them, up to 8.  Where eight do not hold them, 16 for few sequences: one history of 32 771 slots
+  // 28.4 us (with eight 33.7), six 62 (67), but eight of 60 000 101 (96): not all fit the GPU at once;
+  // and 16 000 slots, which eight hold, 23.9 (21.8).
   int S = 1;
-  while (S < SEL_CLUSTER && ((int64_t)S * SEL_THREADS * SEL_KEYS < a.room || 2 * S * a.B <= sms)) S *= 2;
-  const hstu_status_t rc = launch(evict_select_kernel, a.B * S, SEL_THREADS, 0, S, st, a);
+  while (S < 8 && ((int64_t)S * SEL_THREADS * SEL_KEYS < a.room || 2 * S * a.B <= sms)) S *= 2;
+  hstu_status_t rc = HSTU_ERR_CUDA;
+  if (8LL * SEL_THREADS * SEL_KEYS < a.room && 3 * SEL_CLUSTER * a.B <= 2 * sms &&
+      cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess)
+    rc = launch(evict_select_kernel, a.B * SEL_CLUSTER, SEL_THREADS, 0, SEL_CLUSTER, st, a);
+  // (a GPU partition may have no room for 16: nothing was launched then)
+  if (rc != HSTU_OK) rc = launch(evict_select_kernel, a.B * S, SEL_THREADS, 0, S, st, a);
   if (rc != HSTU_OK) return rc;
   // twice what fits the SMs at once, over all sequences; at least one each
   const int64_t ctas = (8LL * sms + a.B - 1) / a.B;
