@@ -1159,10 +1159,12 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
 // Moves the kept rows into the gaps.  Sources lie at or above slot `budget`, destinations below it,
 // so rows move in any order.  LPR lanes of 16 bytes a (token, head), K and V; rows are taken in the
 // order (32 moves, head, move), so that neighbours share a page's part of a head.  HBM-bound, on
-// pieces of 128 bytes or more in no order.
+// pieces of 128 bytes or more in no order: 34 MB read and written in about 14 us.  One piece a thread
+// at a time and all 2048 threads of a SM measured best (two or four pieces, fewer threads: 0.1 to 2 us
+// longer; more CTAs than fit at once: 1 us, all of it their launch).
 template <int LPR>
-__global__ void __launch_bounds__(256, 4) evict_move_kernel(const Evict a, int ctas) {
-  constexpr int R = 256 / LPR, U = 4;
+__global__ void __launch_bounds__(256, 8) evict_move_kernel(const Evict a, int ctas) {
+  constexpr int R = 256 / LPR;
   after_previous();
   const int64_t b = blockIdx.x / ctas;
   const int part = (int)(blockIdx.x % ctas), H = a.c.H, shift = a.c.ps_shift, ps = 1 << shift;
@@ -1170,47 +1172,23 @@ __global__ void __launch_bounds__(256, 4) evict_move_kernel(const Evict a, int c
   const int64_t count = a.count[b], items = (count + 31) / 32 * 32 * H;
   const uint32_t *tos = a.to + b * a.moves, *froms = a.from + b * a.moves;
   uint4 *k = static_cast<uint4*>(a.c.k) + sub, *v = static_cast<uint4*>(a.c.v) + sub;
-  for (int64_t x0 = (int64_t)part * R * U + threadIdx.x / LPR; x0 < items; x0 += (int64_t)ctas * R * U) {
-    uint4 kr[U], vr[U];
-    uint32_t to[U], from[U];   // slots, then rows
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int64_t x = x0 + u * R, m = div_by(x / 32, H) * 32 + x % 32;
-      to[u] = from[u] = ~0u;
-      if (x < items && m < count) {
-        to[u] = tos[m];
-        from[u] = froms[m];
+  for (int64_t x = (int64_t)part * R + threadIdx.x / LPR; x < items; x += (int64_t)ctas * R) {
+    const int64_t g = x / 32, c = div_by(g, H), m = c * 32 + x % 32;
+    if (m >= count) continue;
+    const uint32_t h = (uint32_t)(g - c * H), to = tos[m], from = froms[m];
+    if (to == ~0u || from == ~0u) continue;
+    const uint32_t rt = ((to >> shift) * H + h << shift) + (to & (ps - 1));
+    const uint32_t rf = ((from >> shift) * H + h << shift) + (from & (ps - 1));
+    const uint4 kr = __ldcs(k + (int64_t)rf * LPR), vr = __ldcs(v + (int64_t)rf * LPR);
+    if (sub == 0) {
+      a.c.weights[rt] = a.c.weights[rf];
+      if (h == 0) {
+        a.c.positions[to] = a.c.positions[from];
+        if (a.c.timestamps) a.c.timestamps[to] = a.c.timestamps[from];
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int64_t g = (x0 + u * R) / 32;
-      const uint32_t h = (uint32_t)(g - div_by(g, H) * H);
-      if (to[u] == ~0u || from[u] == ~0u) {
-        to[u] = ~0u;
-        continue;
-      }
-      const uint32_t t = to[u], f = from[u];
-      to[u] = ((t >> shift) * H + h << shift) + (t & (ps - 1));
-      from[u] = ((f >> shift) * H + h << shift) + (f & (ps - 1));
-      if (h == 0 && sub == 0) {
-        a.c.positions[t] = a.c.positions[f];
-        if (a.c.timestamps) a.c.timestamps[t] = a.c.timestamps[f];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; u++)
-      if (to[u] != ~0u) {
-        kr[u] = __ldcs(k + (int64_t)from[u] * LPR);
-        vr[u] = __ldcs(v + (int64_t)from[u] * LPR);
-        if (sub == 0) a.c.weights[to[u]] = a.c.weights[from[u]];
-      }
-#pragma unroll
-    for (int u = 0; u < U; u++)
-      if (to[u] != ~0u) {
-        __stcs(k + (int64_t)to[u] * LPR, kr[u]);
-        __stcs(v + (int64_t)to[u] * LPR, vr[u]);
-      }
+    __stcs(k + (int64_t)rt * LPR, kr);
+    __stcs(v + (int64_t)rt * LPR, vr);
   }
 }
 
@@ -1307,7 +1285,7 @@ inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaSt
   // (a GPU partition may have no room for 16: nothing was launched then)
   if (rc != HSTU_OK) rc = launch(evict_select_kernel, a.B * S, SEL_THREADS, 0, S, st, a);
   if (rc != HSTU_OK) return rc;
-  // twice what fits the SMs at once, over all sequences; at least one each
+  // what fits the SMs at once, over all sequences; at least one each
   const int64_t ctas = (8LL * sms + a.B - 1) / a.B;
   auto kern = row_bytes == 128 ? evict_move_kernel<8> : row_bytes == 256 ? evict_move_kernel<16> : evict_move_kernel<32>;
   return launch(kern, a.B * ctas, 256, 0, 0, st, a, (int)ctas);
