@@ -356,14 +356,27 @@ class PagedCache:
                    z((num_pages, num_heads, page_size), torch.float32, weights))
 
 
-def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, device):
-    """Address of a tensor argument of the paged cache's calls, checked; None for None."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.get_device() == device.index:
-        return t.data_ptr()
+def _refuse(name: str, t: torch.Tensor, dtype, numel: int, device):
     raise ValueError(f"{name}: a contiguous {dtype} tensor of {numel} elements on {device} is wanted, "
                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, device):
+    """Address of a tensor argument of the paged cache's calls, checked; None for None."""
+    return _args(device, ((name, t, dtype, numel),))[0]
+
+
+def _args(device, wanted):
+    """Addresses of several (name, tensor, dtype, elements), checked."""
+    index, out = device.index, []
+    for name, t, dtype, numel in wanted:
+        if t is None:
+            out.append(None)
+        elif t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.get_device() == index:
+            out.append(t.data_ptr())
+        else:
+            _refuse(name, t, dtype, numel, device)
+    return out
 
 
 def _call(fn, what: str, device, stream, *args) -> None:
@@ -375,8 +388,7 @@ def _call(fn, what: str, device, stream, *args) -> None:
         stream = torch._C._cuda_getCurrentRawStream(index)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    now = torch.cuda.current_device()
-    if now == index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -385,44 +397,44 @@ def _call(fn, what: str, device, stream, *args) -> None:
         raise HstuError(rc, what)
 
 
-def _table(cache: PagedCache, page_table, cache_lens, next_positions):
+def _new(shape, dtype, device, stream):
+    """A tensor that the call's stream may use and, once it is released, reuse."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(page_table):
     if page_table.dim() != 2:
         raise ValueError("page_table is [num_seqs, max_pages]")
-    B, M = page_table.shape
-    dev = cache.device
-    return B, M, (_arg("page_table", page_table, torch.int32, B * M, dev),
-                  _arg("cache_lens", cache_lens, torch.int64, B, dev),
-                  _arg("next_positions", next_positions, torch.int64, B, dev))
+    return page_table.shape
 
 
-def _space(workspace, size, device):
+def _space(workspace, size, device, stream):
     """The workspace to use: the caller's (any contiguous tensor on the device) or a new one."""
     if workspace is None:
-        return torch.empty(max(256, size()), dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
+        return _new(max(256, size()), torch.uint8, device, stream)
+    if workspace.get_device() != device.index or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on {device} is wanted")
     return workspace
-
-
-def _biases(shape: HstuShape, pos_table, time_table, alibi_slopes, device):
-    H, f = shape.num_heads, torch.float32
-    return (_arg("pos_table", pos_table, f, H * shape.n_pos_buckets, device),
-            _arg("time_table", time_table, f, H * shape.n_time_buckets, device),
-            _arg("alibi_slopes", alibi_slopes, f, H, device))
 
 
 def hstu_cache_append(cache: PagedCache, uvqk, seq_offsets, timestamps, page_table, cache_lens,
                       next_positions=None, stream=None) -> None:
     """The K and V rows of a jagged U|V|Q|K batch into the cache (see the C header); cache_lens is
     the caller's to advance."""
-    B, M, (tp, lp, np_) = _table(cache, page_table, cache_lens, next_positions)
-    n1, dev = 4 * cache.num_heads * cache.head_dim, cache.device
-    T = int(uvqk.shape[0])
-    up = _arg("uvqk", uvqk, cache.k.dtype, T * n1, dev)
-    op = _arg("seq_offsets", seq_offsets, torch.int64, B + 1, dev)
-    sp = _arg("timestamps", timestamps, torch.int64, T, dev)
-    _call(_lib.hstu_cache_append, "hstu_cache_append", dev, stream, cache.ref, B, T, up, op, sp, tp,
-          M, lp, np_)
+    B, M = _rows(page_table)
+    T, i64 = int(uvqk.shape[0]), torch.int64
+    _call(_lib.hstu_cache_append, "hstu_cache_append", cache.device, stream, cache.ref, B, T,
+          *_args(cache.device, (
+              ("uvqk", uvqk, cache.k.dtype, T * 4 * cache.num_heads * cache.head_dim),
+              ("seq_offsets", seq_offsets, i64, B + 1), ("timestamps", timestamps, i64, T),
+              ("page_table", page_table, torch.int32, B * M))), M,
+          *_args(cache.device, (("cache_lens", cache_lens, i64, B),
+                                ("next_positions", next_positions, i64, B))))
 
 
 def paged_attention_workspace_size(shape: HstuShape) -> int:
@@ -434,15 +446,18 @@ def hstu_paged_attention_fwd(shape: HstuShape, cache: PagedCache, uvqk, page_tab
                              scale: float, av, append: bool = True, workspace=None, stream=None):
     """Attention of one new token a sequence over its cached tokens and itself (see the C header);
     with `append` the token joins the cache.  Fills and returns av [B, H*hd] (fp32)."""
-    B, M, (tp, lp, np_) = _table(cache, page_table, cache_lens, next_positions)
-    w, dev = cache.num_heads * cache.head_dim, cache.device
+    B, M = _rows(page_table)
+    w, dev, i64, f32 = cache.num_heads * cache.head_dim, cache.device, torch.int64, torch.float32
     if shape.num_seqs != B:
         raise ValueError(f"page_table has {B} rows, the shape {shape.num_seqs} sequences")
-    up = _arg("uvqk", uvqk, cache.k.dtype, B * 4 * w, dev)
-    sp = _arg("timestamps", timestamps, torch.int64, B, dev)
-    ap = _arg("av", av, torch.float32, B * w, dev)
-    pos, tim, ali = _biases(shape, pos_table, time_table, alibi_slopes, dev)
-    ws = _space(workspace, lambda: paged_attention_workspace_size(shape), dev)
+    H = shape.num_heads
+    up, tp, lp, np_, sp, pos, tim, ali, ap = _args(dev, (
+        ("uvqk", uvqk, cache.k.dtype, B * 4 * w), ("page_table", page_table, torch.int32, B * M),
+        ("cache_lens", cache_lens, i64, B), ("next_positions", next_positions, i64, B),
+        ("timestamps", timestamps, i64, B), ("pos_table", pos_table, f32, H * shape.n_pos_buckets),
+        ("time_table", time_table, f32, H * shape.n_time_buckets),
+        ("alibi_slopes", alibi_slopes, f32, H), ("av", av, f32, B * w)))
+    ws = _space(workspace, lambda: paged_attention_workspace_size(shape), dev, stream)
     _call(_lib.hstu_paged_attention_fwd, "hstu_paged_attention_fwd", dev, stream, ctypes.byref(shape),
           cache.ref, up, tp, M, lp, np_, sp, pos, tim, ali, scale, 1 if append else 0, ap,
           ws.data_ptr(), ws.nbytes)
@@ -458,20 +473,22 @@ def hstu_paged_layer_fwd(shape: HstuShape, cache: PagedCache, X, page_table, cac
                          time_table, alibi_slopes, scale: float, out=None, append: bool = True,
                          workspace=None, stream=None):
     """One HSTU layer over one new token a sequence, against the layer's paged cache."""
-    B, M, (tp, lp, np_) = _table(cache, page_table, cache_lens, next_positions)
+    B, M = _rows(page_table)
     w, d, dt, dev = cache.num_heads * cache.head_dim, shape.d_model, cache.k.dtype, cache.device
     if shape.num_seqs != B:
         raise ValueError(f"page_table has {B} rows, the shape {shape.num_seqs} sequences")
     if out is None:
-        out = torch.empty_like(X)
-    xp = _arg("X", X, dt, B * d, dev)
-    weights = [_arg("W1", W1, dt, d * 4 * w, dev), _arg("b1", b1, dt, 4 * w, dev),
-               _arg("W2", W2, dt, w * d, dev), _arg("b2", b2, dt, d, dev),
-               _arg("ln_w", ln_w, dt, w, dev), _arg("ln_b", ln_b, dt, w, dev)]
-    sp = _arg("timestamps", timestamps, torch.int64, B, dev)
-    pos, tim, ali = _biases(shape, pos_table, time_table, alibi_slopes, dev)
-    op = _arg("out", out, dt, B * d, dev)
-    ws = _space(workspace, lambda: paged_layer_workspace_size(shape), dev)
+        out = _new(X.shape, dt, dev, stream)
+    H, i64, f32 = shape.num_heads, torch.int64, torch.float32
+    xp, tp, lp, np_, sp, pos, tim, ali, op, *weights = _args(dev, (
+        ("X", X, dt, B * d), ("page_table", page_table, torch.int32, B * M),
+        ("cache_lens", cache_lens, i64, B), ("next_positions", next_positions, i64, B),
+        ("timestamps", timestamps, i64, B), ("pos_table", pos_table, f32, H * shape.n_pos_buckets),
+        ("time_table", time_table, f32, H * shape.n_time_buckets),
+        ("alibi_slopes", alibi_slopes, f32, H), ("out", out, dt, B * d),
+        ("W1", W1, dt, d * 4 * w), ("b1", b1, dt, 4 * w), ("W2", W2, dt, w * d), ("b2", b2, dt, d),
+        ("ln_w", ln_w, dt, w), ("ln_b", ln_b, dt, w)))
+    ws = _space(workspace, lambda: paged_layer_workspace_size(shape), dev, stream)
     _call(_lib.hstu_paged_layer_fwd, "hstu_paged_layer_fwd", dev, stream, ctypes.byref(shape),
           cache.ref, xp, tp, M, lp, np_, sp, *weights, pos, tim, ali, scale, 1 if append else 0, op,
           ws.data_ptr(), ws.nbytes)
@@ -486,12 +503,14 @@ def hstu_cache_evict(cache: PagedCache, page_table, cache_lens, next_positions, 
                      recent: int, new_lens=None, workspace=None, stream=None):
     """Cuts sequences above `budget` cached tokens to their `recent` newest and the most attended of
     the others (see the C header).  Returns new_lens [B] (cache_lens itself is allowed)."""
-    B, M, (tp, lp, np_) = _table(cache, page_table, cache_lens, next_positions)
-    dev = cache.device
+    B, M = _rows(page_table)
+    dev, i64 = cache.device, torch.int64
     if new_lens is None:
-        new_lens = torch.empty_like(cache_lens)
-    ep = _arg("new_lens", new_lens, torch.int64, B, dev)
-    ws = _space(workspace, lambda: cache_evict_workspace_size(cache, B, M), dev)
+        new_lens = _new(B, i64, dev, stream)
+    tp, lp, np_, ep = _args(dev, (
+        ("page_table", page_table, torch.int32, B * M), ("cache_lens", cache_lens, i64, B),
+        ("next_positions", next_positions, i64, B), ("new_lens", new_lens, i64, B)))
+    ws = _space(workspace, lambda: cache_evict_workspace_size(cache, B, M), dev, stream)
     _call(_lib.hstu_cache_evict, "hstu_cache_evict", dev, stream, cache.ref, B, tp, M, lp, np_, budget,
           recent, ep, ws.data_ptr(), ws.nbytes)
     return new_lens

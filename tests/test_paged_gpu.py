@@ -286,6 +286,27 @@ def test_attention_on_two_streams_at_once(hstu):
         check_av(g["av"], c.want_attention()[0], c.bounds()[0])
 
 
+def test_calls_on_a_stream_of_their_own_allocate_there(hstu):
+    # new workspaces and outputs belong to the call's stream, given as an object or as its address
+    c = Case(30, [400, 90], 4, 64, 16, extra=4)
+    st, busy = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    for address in (False, True):
+        g = c.on_device(hstu)
+        torch.cuda.synchronize()
+        stream = st.cuda_stream if address else st
+        with torch.cuda.stream(st):
+            for _ in range(3):
+                busy = busy @ busy * 1e-3                    # the stream is behind the host
+        c.attend(hstu, g, append=False, stream=stream)
+        for _ in range(8):                                   # what the current stream allocates meanwhile
+            torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+        new = hstu.hstu_cache_evict(g["cache"], g["table"], g["lens"], g["next"], 64, 8, stream=stream)
+        torch.cuda.synchronize()
+        assert hstu.device_status() == hstu.HSTU_OK
+        check_av(g["av"], c.want_attention(append=False)[0], c.bounds()[0])
+        assert new.tolist() == [64, 64]
+
+
 # ------------------------------------------------------------------------------------------------
 # Append
 # ------------------------------------------------------------------------------------------------
