@@ -838,8 +838,8 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
 }
 
 // Selection, one cluster of CTAs per sequence, each on a contiguous part of its slots, each warp on a
-// contiguous part of that.  Every thread scores its slots; the first SEL_KEYS keys stay in registers,
-// any further ones go through the workspace.  The budget-th largest key is found by histograms of the
+// contiguous part of that.  Every thread scores its slots; the first SEL_ROUNDS keys stay in shared
+// memory, any further ones go through the workspace.  The budget-th largest key is found by histograms of the
 // top 11, the next 11 and the last 10 bits: every CTA counts its own keys, sums all CTAs' bins
 // through distributed shared memory and finds the bin for itself; once few keys share the bits found
 // so far, every CTA gathers those and finishes alone, with one cluster barrier a step.  Then every
@@ -847,11 +847,14 @@ __device__ __forceinline__ uint32_t weight_key(float s) {
 // order.  Eleven bits (two of the mantissa) spread accumulated weights over enough bins that the
 // shared-memory atomics seldom meet; warps whose keys all fall into one bin add them at once.
 //
-// Bound by latency: 8 sequences of 8192 slots and 8 heads take 20 600 clocks (10.7 us): the scores
-// 7400, the search 9100 (two passes), the lists 4100.  Hence several CTAs a sequence (with one, 19 us)
-// and 512 threads (256: 5 us longer for 32 771 slots).  Exchanging whole histograms through distributed shared memory took 2 us longer.
+// Bound by latency and by fetching instructions that run a few times: 8 sequences of 8192 slots and 8
+// heads take about 10 us (scores 3.8, search 4.5 in two passes, lists 2).  Hence several CTAs a
+// sequence (with one, 8 us longer), 512 threads (256: 5 us longer for 32 771 slots), and loops over
+// keys in shared memory (unrolled over registers: 16 000 slots 21.9 us an eviction, so 20.1).
+// Exchanging whole histograms through distributed shared memory took 2 us longer.
 constexpr int SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32, SEL_KEYS = 8, SEL_CLUSTER = 16;
-constexpr int SEL_BINS = 2048, SEL_LIST = 1024;
+constexpr int SEL_BINS = 2048, SEL_LIST = 1024, SEL_ROUNDS = 16;
+constexpr int SEL_SMEM = 2 * SEL_ROUNDS * SEL_THREADS * 4;   // keys and pages of a thread's slots
 
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a) {
   namespace cg = cooperative_groups;
@@ -864,7 +867,9 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   __shared__ int s_count[3][SEL_CLUSTER];      // equal keys, gaps and movers of the cluster's CTAs
   __shared__ int s_found[3];                   // the bin that holds the key searched, how many of its
                                                // keys are kept, and how many there are
+  extern __shared__ uint32_t s_own[];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  uint32_t *const s_key = s_own + tid, *const s_page = s_key + SEL_ROUNDS * SEL_THREADS;
   if (tid == 0) s_listed = 0;
   for (int i = tid; i < 3 * SEL_BINS / 4; i += SEL_THREADS)
     reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
@@ -892,7 +897,6 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
 
   // scores: the loads of SEL_KEYS slots and four heads are in flight at once
   // (unconditional, from some slot where there is none: a load under a condition is waited for at once)
-  uint32_t key[SEL_KEYS], page[SEL_KEYS];
 #pragma unroll 1
   for (int r0 = 0; r0 < rounds; r0 += SEL_KEYS) {
     uint32_t at[SEL_KEYS];      // rows of weights: below 2^32
@@ -912,7 +916,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
         if (at[i] < (uint32_t)a.c.num_pages) live |= 1u << i;
         else report(HSTU_ERR_DEVICE_BAD_OFFSETS);
       }
-      if (r0 == 0) page[i] = live >> i & 1 ? at[i] : ~0u;
+      if (r0 + i < SEL_ROUNDS) s_page[(r0 + i) * SEL_THREADS] = live >> i & 1 ? at[i] : ~0u;
       if (!(live >> i & 1)) at[i] = 0;   // any page: the value is dropped
       const int o = j & (ps - 1);
       pos[i] = a.c.positions[((int64_t)at[i] << shift) + o];
@@ -936,28 +940,26 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       const int j = start + (r0 + i) * 32;
       uint32_t k = (int64_t)pos[i] >= oldest ? KEY_RECENT : weight_key((float)sum[i]);
       if (!(live >> i & 1)) k = 0;         // a slot of no page goes first, and nothing moves for it
-      if (r0 == 0) key[i] = k;
+      if (r0 + i < SEL_ROUNDS) s_key[(r0 + i) * SEL_THREADS] = k;
       else if (r0 + i < rounds && j < n) spill[j] = k;
     }
   }
   // f(slot, key, its page or some page, whether there is such a slot) for the warp's slots in order;
-  // all lanes take part
-  auto each = [&](auto f, bool pages_too = false) {
-#pragma unroll
-    for (int i = 0; i < SEL_KEYS; i++)
-      if (i < rounds) f(start + i * 32, key[i], page[i], start + i * 32 < n);
+  // all lanes take part.  Not unrolled: what runs a few times is bound by fetching its instructions.
+  auto each = [&](auto f) {
 #pragma unroll 1
-    for (int r0 = SEL_KEYS; r0 < rounds; r0 += SEL_KEYS) {
-      uint32_t k[SEL_KEYS], pg[SEL_KEYS];
-#pragma unroll
-      for (int i = 0; i < SEL_KEYS; i++) {
-        const int j = start + (r0 + i) * 32, at = j < n ? j : n - 1;
-        k[i] = spill[at];
-        pg[i] = pages_too ? (uint32_t)pages[at >> shift] : 0u;
+    for (int r = 0; r < rounds; r++) {
+      const int j = start + r * 32;
+      uint32_t k, pg;
+      if (r < SEL_ROUNDS) {
+        k = s_key[r * SEL_THREADS];
+        pg = s_page[r * SEL_THREADS];
+      } else {
+        const int at = j < n ? j : n - 1;
+        k = spill[at];
+        pg = (uint32_t)pages[at >> shift];
       }
-#pragma unroll
-      for (int i = 0; i < SEL_KEYS; i++)
-        if (r0 + i < rounds) f(start + (r0 + i) * 32, k[i], pg[i], start + (r0 + i) * 32 < n);
+      f(j, k, pg, j < n);
     }
   };
   __syncthreads();   // bins are zero
@@ -1106,7 +1108,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
     equal += before_cta(0);
   }
   // f(slot, its page, lanes whose slot is a gap, lanes whose slot moves) for the warp's slots in order
-  auto each_flagged = [&](auto f, bool pages_too) {
+  auto each_flagged = [&](auto f) {
     int seen = equal;
     each([&](int j, uint32_t k, uint32_t pg, bool in) {
       bool keep = in && k >= prefix;
@@ -1117,13 +1119,13 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
       }
       f(j, k, pg, __ballot_sync(0xffffffffu, in && j < budget && !keep),
         __ballot_sync(0xffffffffu, in && j >= budget && keep));
-    }, pages_too);
+    });
   };
   int gaps = 0, movers = 0;
   each_flagged([&](int, uint32_t, uint32_t, unsigned g, unsigned m) {
     gaps += __popc(g);
     movers += __popc(m);
-  }, false);
+  });
   if (lane == 0) {
     s_gaps[warp] = gaps;
     s_movers[warp] = movers;
@@ -1152,7 +1154,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
     }
     gap_at += __popc(g);
     mover_at += __popc(m);
-  }, true);
+  });
   // (nobody has touched another CTA's shared memory since the last sync: each may leave)
 }
 
@@ -1272,18 +1274,20 @@ inline hstu_status_t launch_append(const Cache& c, int row_bytes, int64_t T, int
 }
 
 inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaStream_t st) {
-  // As many CTAs as hold the keys of a row's slots in registers, and more while there are SMs for
-  // them, up to 8.  Where eight do not hold them, 16 for few sequences: one history of 32 771 slots
-  // 28.4 us (with eight 33.7), six 62 (67), but eight of 60 000 101 (96): not all fit the GPU at once;
-  // and 16 000 slots, which eight hold, 23.9 (21.8).
+  // As many CTAs as hold the keys of a row's slots, and more while there are SMs for them, up to 8.
+  // Above 4096 slots a CTA of eight, 16 for few sequences: one history of 32 771 slots 28.4 us (with
+  // eight 33.7), six 62 (67), but eight of 60 000 101 (96): not all fit the GPU at once; and 16 000
+  // slots 23.9 (21.8).
   int S = 1;
-  while (S < 8 && ((int64_t)S * SEL_THREADS * SEL_KEYS < a.room || 2 * S * a.B <= sms)) S *= 2;
+  while (S < 8 && ((int64_t)S * SEL_THREADS * SEL_ROUNDS < a.room || 2 * S * a.B <= sms)) S *= 2;
   hstu_status_t rc = HSTU_ERR_CUDA;
+  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_SMEM) != cudaSuccess)
+    return rc;
   if (8LL * SEL_THREADS * SEL_KEYS < a.room && 3 * SEL_CLUSTER * a.B <= 2 * sms &&
       cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess)
-    rc = launch(evict_select_kernel, a.B * SEL_CLUSTER, SEL_THREADS, 0, SEL_CLUSTER, st, a);
+    rc = launch(evict_select_kernel, a.B * SEL_CLUSTER, SEL_THREADS, SEL_SMEM, SEL_CLUSTER, st, a);
   // (a GPU partition may have no room for 16: nothing was launched then)
-  if (rc != HSTU_OK) rc = launch(evict_select_kernel, a.B * S, SEL_THREADS, 0, S, st, a);
+  if (rc != HSTU_OK) rc = launch(evict_select_kernel, a.B * S, SEL_THREADS, SEL_SMEM, S, st, a);
   if (rc != HSTU_OK) return rc;
   // what fits the SMs at once, over all sequences; at least one each
   const int64_t ctas = (8LL * sms + a.B - 1) / a.B;

@@ -407,9 +407,11 @@ def test_evict_a_long_history(hstu):
 
 
 @pytest.mark.parametrize("kind", ["random", "zero", "two values"])
-def test_evict_histories_beyond_the_registers(hstu, kind):
-    # more slots than a cluster of eight CTAs keeps in registers: keys go through the workspace
-    c = Case(48, [70001, 100], 1, 64, 1024, bias="none")
+@pytest.mark.parametrize("others", [1, 9])
+def test_evict_long_histories(hstu, kind, others):
+    # few sequences: a cluster of sixteen CTAs; more of them: eight, whose shared memory does not hold
+    # all keys, so that some go through the workspace
+    c = Case(48, [70001] + [100] * others, 1, 64, 1024, bias="none")
     live = ~np.isnan(c.cache["weights"])
     if kind != "random":
         c.cache["weights"][live] = 0.0 if kind == "zero" else c.rng.integers(0, 2, live.sum())
