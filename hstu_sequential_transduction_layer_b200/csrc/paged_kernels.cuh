@@ -828,6 +828,10 @@ struct Evict {
 
 constexpr uint32_t KEY_RECENT = 0xffffffffu;
 
+// The two halves of a cluster barrier; the first publishes nothing.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 // Keys that order tokens by what is kept first: recent ones, then by weight (sums rounded once to
 // fp32; NaN last), as unsigned integers.
 __device__ __forceinline__ uint32_t weight_key(float s) {
@@ -883,6 +887,9 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
     }
     return;
   }
+  // the CTAs store to each other from the search's first step on: by then all of them have to have
+  // started, which the scoring leaves time for
+  if (S > 1) cluster_arrive();
   auto sync = [&]() {
     if (S > 1) cluster.sync(); else __syncthreads();
   };
@@ -963,6 +970,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
     }
   };
   __syncthreads();   // bins are zero
+  if (S > 1) cluster_wait();
 
   uint32_t prefix = 0, mask = 0;
   int want = budget;          // of the keys that share the prefix, how many are kept
