@@ -1206,6 +1206,14 @@ __global__ void __launch_bounds__(256, 8) evict_move_kernel(const Evict a, int c
 // Launchers (arguments already checked)
 // ------------------------------------------------------------------------------------------------
 
+// Whether a runtime call succeeded.  A failed call's error is taken back, so that no later check of
+// the last error meets it; an error that some earlier call left is neither looked at nor touched.
+inline bool succeeded(cudaError_t e) {
+  if (e == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 // Launches a kernel of this file (see after_previous), `cluster` CTAs a cluster.
 template <typename... P, typename... A>
 hstu_status_t launch(void (*kern)(P...), int64_t grid, int threads, int smem, int cluster, cudaStream_t st,
@@ -1223,8 +1231,7 @@ hstu_status_t launch(void (*kern)(P...), int64_t grid, int threads, int smem, in
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = cluster ? 2 : 1;
-  const bool ok = cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess;
-  if (cudaGetLastError() != cudaSuccess || !ok) return HSTU_ERR_CUDA;
+  if (!succeeded(cudaLaunchKernelEx(&cfg, kern, P(args)...))) return HSTU_ERR_CUDA;
   count_launch();
   return HSTU_OK;
 }
@@ -1250,7 +1257,7 @@ hstu_status_t launch_attention_t(const Attn& a, void* ws, int sms, cudaStream_t 
   float* parts = static_cast<float*>(ws);
   Part* recs = reinterpret_cast<Part*>(parts + (size_t)ATTN_MAX_CTAS * 2 * HD);
   auto kern = attention_kernel<T, HD>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
+  if (!succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)))
     return HSTU_ERR_CUDA;
   const hstu_status_t rc = launch(kern, grid, ATTN_THREADS, SMEM, 0, st, a, parts, recs);
   // one CTA joins its warps' parts itself, and a single tile a (sequence, head) has no parts
@@ -1281,6 +1288,32 @@ inline hstu_status_t launch_append(const Cache& c, int row_bytes, int64_t T, int
                 static_cast<const uint4*>(uvqk), off, ts, table, max_pages, lens, next_pos);
 }
 
+// Allows the selection clusters of SEL_CLUSTER CTAs, which are more than every device has to offer;
+// says whether the current device has room for one (a GPU partition may not).  That is asked once a
+// device, and before anything is launched; the permission belongs to the context and is given anew.
+inline bool wide_clusters_fit() {
+  static std::atomic<int> known[64];   // 0: not asked yet, 1: no, 2: yes
+  int dev = 0, clusters = 0;
+  if (!succeeded(cudaGetDevice(&dev)) ||
+      !succeeded(cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)))
+    return false;
+  std::atomic<int>* slot = dev < 64 ? &known[dev] : nullptr;
+  if (slot && slot->load()) return slot->load() == 2;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = SEL_CLUSTER;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(SEL_CLUSTER);
+  cfg.blockDim = dim3(SEL_THREADS);
+  cfg.dynamicSmemBytes = SEL_SMEM;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const bool fit = succeeded(cudaOccupancyMaxActiveClusters(&clusters, evict_select_kernel, &cfg)) && clusters > 0;
+  if (slot) slot->store(fit ? 2 : 1);
+  return fit;
+}
+
 inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaStream_t st) {
   // As many CTAs as hold the keys of a row's slots, and more while there are SMs for them, up to 8.
   // Above 4096 slots a CTA of eight, 16 for few sequences: one history of 32 771 slots 28.4 us (with
@@ -1288,14 +1321,11 @@ inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaSt
   // slots 23.9 (21.8).
   int S = 1;
   while (S < 8 && ((int64_t)S * SEL_THREADS * SEL_ROUNDS < a.room || 2 * S * a.B <= sms)) S *= 2;
-  hstu_status_t rc = HSTU_ERR_CUDA;
-  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_SMEM) != cudaSuccess)
-    return rc;
-  if (8LL * SEL_THREADS * SEL_KEYS < a.room && 3 * SEL_CLUSTER * a.B <= 2 * sms &&
-      cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess)
-    rc = launch(evict_select_kernel, a.B * SEL_CLUSTER, SEL_THREADS, SEL_SMEM, SEL_CLUSTER, st, a);
-  // (a GPU partition may have no room for 16: nothing was launched then)
-  if (rc != HSTU_OK) rc = launch(evict_select_kernel, a.B * S, SEL_THREADS, SEL_SMEM, S, st, a);
+  if (!succeeded(cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_SMEM)))
+    return HSTU_ERR_CUDA;
+  if (8LL * SEL_THREADS * SEL_KEYS < a.room && 3 * SEL_CLUSTER * a.B <= 2 * sms && wide_clusters_fit())
+    S = SEL_CLUSTER;
+  const hstu_status_t rc = launch(evict_select_kernel, a.B * S, SEL_THREADS, SEL_SMEM, S, st, a);
   if (rc != HSTU_OK) return rc;
   // what fits the SMs at once, over all sequences; at least one each
   const int64_t ctas = (8LL * sms + a.B - 1) / a.B;

@@ -475,7 +475,8 @@ hstu_status_t hstu_paged_layer_fwd(const hstu_shape_t* shape, const hstu_paged_c
  *                 be cache_lens itself
  *  workspace      hstu_cache_evict_workspace_size(cache, num_seqs, max_pages) bytes, 256-byte aligned
  * The cache needs positions and weights.  The result does not depend on the order of anything that
- * runs.  Asynchronous on `stream`.
+ * runs.  Asynchronous on `stream`.  After HSTU_ERR_CUDA (a launch failed) the cache and new_lens are
+ * undefined.
  */
 size_t hstu_cache_evict_workspace_size(const hstu_paged_cache_t* cache, int64_t num_seqs,
                                        int64_t max_pages);

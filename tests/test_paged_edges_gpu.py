@@ -2,15 +2,20 @@
 work, behind a CUDA error of an earlier call, with rows that name no page, without the optional
 arrays, and with many tiles of one history a warp.  Against the fp64 oracle (oracle/paged.py)."""
 import copy
+import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
 import torch
 
 from oracle import paged
-from tests.paged_util import Case, check_cache, same
+from tests.paged_util import Case, check_av, check_cache, same, values
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -37,3 +42,76 @@ def test_evict_behind_other_work(hstu, lens, ps, budget):
         assert hstu.device_status() == hstu.HSTU_OK
         same(got, new, "new_lens")
         check_cache(g["cache"], want.cache)
+
+
+def leave_an_error(hstu):
+    """Leaves a CUDA error of an earlier call behind in the library's runtime: its status is asked for
+    on a stream that is being captured, which CUDA refuses (and the capture is given up)."""
+    cuda, graph = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    handle = ctypes.c_void_p(st.cuda_stream)
+    assert cuda.cuStreamBeginCapture_v2(handle, 1) == 0                  # 1: this thread's calls
+    assert hstu.library().hstu_get_device_status(handle) == hstu.HSTU_ERR_CUDA
+    assert cuda.cuStreamEndCapture(handle, ctypes.byref(graph)) != 0
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("lens,ps,budget", [([40000, 60], 1024, 20000), ([900, 40, 1000], 16, 500)])
+def test_evict_behind_an_earlier_error(hstu, lens, ps, budget):
+    # one selection only: a second one would find the lengths cut (cache_lens are the new ones) and
+    # leave the kept tokens where they are
+    c = Case(72, lens, 1, 64, ps, bias="none")
+    g = c.on_device(hstu)
+    leave_an_error(hstu)
+    before = hstu.launch_count()
+    hstu.hstu_cache_evict(g["cache"], g["table"], g["lens"], g["next"], budget, 100, new_lens=g["lens"])
+    assert hstu.launch_count() - before == 2
+    assert hstu.device_status() == hstu.HSTU_OK
+    same(g["lens"], paged.evict(c.cache, c.table, c.lens, c.next, budget, 100), "lengths")
+    check_cache(g["cache"], c.cache)
+
+
+def test_attention_and_append_behind_an_earlier_error(hstu):
+    c = Case(73, [100, 700], 2, 64, 16, extra=2)
+    av, want = c.want_attention()
+    ab, wb = c.bounds()
+    g = c.on_device(hstu)
+    leave_an_error(hstu)
+    c.attend(hstu, g)
+    check_av(g["av"], av, ab)
+    check_cache(g["cache"], want, wb)
+    c.cache, weights = want, g["cache"].weights.double().cpu().numpy()
+    c.cache["weights"] = weights
+    rows, off, ts = values(c.rng, (2, 512), "bf16"), np.array([0, 1, 2]), np.array([7, 9])
+    leave_an_error(hstu)
+    hstu.hstu_cache_append(g["cache"], c.dev(rows, torch.bfloat16), c.dev(off, torch.int64),
+                           c.dev(ts, torch.int64), g["table"], g["lens"] + 1, g["next"] + 1)
+    assert hstu.device_status() == hstu.HSTU_OK
+    paged.append(c.cache, rows, off, ts, c.table, c.lens + 1, c.next + 1)
+    check_cache(g["cache"], c.cache)
+
+
+def test_evict_a_long_history_captured_first(hstu):
+    # in a process of its own: nothing has been asked of the device before the capture
+    code = """
+import numpy as np, torch
+import hstu_sequential_transduction_layer_b200 as hstu
+from oracle import paged
+from tests.paged_util import Case, check_cache, same
+c = Case(74, [40000], 1, 64, 1024, bias="none")
+g = c.on_device(hstu)
+ws = torch.empty(hstu.cache_evict_workspace_size(g["cache"], 1, c.M), dtype=torch.uint8, device="cuda")
+graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(graph, stream=st):
+    hstu.hstu_cache_evict(g["cache"], g["table"], g["lens"], g["next"], 9000, 100, new_lens=g["lens"],
+                          workspace=ws)
+graph.replay()
+torch.cuda.synchronize()
+assert hstu.device_status() == hstu.HSTU_OK
+same(g["lens"], paged.evict(c.cache, c.table, c.lens, c.next, 9000, 100), "lengths")
+check_cache(g["cache"], c.cache)
+print("done")
+"""
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "done", out.stderr[-2000:]
