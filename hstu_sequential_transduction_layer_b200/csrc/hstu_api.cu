@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <type_traits>
 #include <vector>
@@ -382,6 +383,23 @@ bool overlaps_cache(const void* p, size_t n, const hstu_paged_cache_t& c) {
          overlaps(p, n, c.weights, slots * c.num_heads * sizeof(float));
 }
 
+// An array that a call only reads: `count` elements of `size` bytes, naturally aligned; or none.
+struct ReadOnly {
+  const void* p;
+  size_t count, size;
+  bool aligned() const { return reinterpret_cast<uintptr_t>(p) % size == 0; }
+  bool meets(const void* q, size_t n) const { return overlaps(q, n, p, count * size); }
+};
+
+// Are the arrays aligned, and apart from the cache and from the two ranges that a call writes?
+bool apart(std::initializer_list<ReadOnly> arrays, const hstu_paged_cache_t& c, const void* out = nullptr,
+           size_t out_bytes = 0, const void* ws = nullptr, size_t ws_bytes = 0) {
+  for (const ReadOnly& a : arrays)
+    if (!a.aligned() || a.meets(out, out_bytes) || a.meets(ws, ws_bytes) || overlaps_cache(a.p, a.count * a.size, c))
+      return false;
+  return true;
+}
+
 paged::Cache cache_view(const hstu_paged_cache_t& c) {
   int shift = 0;
   while ((1 << shift) < c.page_size) shift++;
@@ -444,6 +462,17 @@ hstu_status_t run_paged_attention(const hstu_shape_t& s, const hstu_paged_cache_
   a.max_len = s.max_seq_len - 1;
   a.av = (float*)av;
   return paged::launch_attention(a, s.dtype, s.d_qk, ws, tc::num_sms(), st);
+}
+
+// The same for what the attention reads besides U|V|Q|K and the cache.
+bool paged_inputs_apart(const hstu_shape_t& s, const hstu_paged_cache_t& cache, const int32_t* page_table,
+                        int64_t max_pages, const int64_t* cache_lens, const int64_t* next_positions,
+                        const int64_t* timestamps, const float* pos, const float* tim, const float* alibi,
+                        const void* out, size_t out_bytes, const void* ws, size_t ws_bytes) {
+  const size_t B = (size_t)s.num_seqs, H = (size_t)s.num_heads;
+  return apart({{page_table, B * max_pages, 4}, {cache_lens, B, 8}, {next_positions, B, 8}, {timestamps, B, 8},
+                {pos, H * s.n_pos_buckets, 4}, {tim, H * s.n_time_buckets, 4}, {alibi, H, 4}},
+               cache, out, out_bytes, ws, ws_bytes);
 }
 
 struct PagedWorkspace {
@@ -1079,7 +1108,11 @@ hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seq
   if (total_tokens == 0) return HSTU_OK;
   if (num_seqs == 0 || !uvqk || !seq_offsets || !aligned16(uvqk)) return HSTU_ERR_INVALID_ARG;
   if (cache->timestamps && !timestamps) return HSTU_ERR_INVALID_ARG;
-  if (overlaps_cache(uvqk, (size_t)total_tokens * 4 * cache->num_heads * row_bytes(*cache), *cache))
+  const size_t B = (size_t)num_seqs, T = (size_t)total_tokens;
+  if (overlaps_cache(uvqk, T * 4 * cache->num_heads * row_bytes(*cache), *cache) ||
+      !apart({{seq_offsets, B + 1, 8}, {timestamps, T, 8}, {page_table, B * max_pages, 4}, {cache_lens, B, 8},
+              {next_positions, B, 8}},
+             *cache))
     return HSTU_ERR_INVALID_ARG;
   return paged::launch_append(cache_view(*cache), row_bytes(*cache), total_tokens, num_seqs, uvqk,
                               seq_offsets, timestamps, page_table, max_pages, cache_lens,
@@ -1110,7 +1143,9 @@ hstu_status_t hstu_paged_attention_fwd(const hstu_shape_t* shape, const hstu_pag
   const size_t avb = (size_t)s.num_seqs * wv_of(s) * 4, ub = (size_t)s.num_seqs * n1_of(s) * esize(s);
   if (overlaps(av, avb, uvqk, ub) || overlaps(av, avb, workspace, workspace_bytes) ||
       overlaps(uvqk, ub, workspace, workspace_bytes) || overlaps_cache(av, avb, *cache) ||
-      overlaps_cache(uvqk, ub, *cache) || overlaps_cache(workspace, workspace_bytes, *cache))
+      overlaps_cache(uvqk, ub, *cache) || overlaps_cache(workspace, workspace_bytes, *cache) ||
+      !paged_inputs_apart(s, *cache, page_table, max_pages, cache_lens, next_positions, timestamps, pos_table,
+                          time_table, alibi_slopes, av, avb, workspace, workspace_bytes))
     return HSTU_ERR_INVALID_ARG;
   return run_paged_attention(s, *cache, uvqk, page_table, max_pages, cache_lens, next_positions,
                              timestamps, pos_table, time_table, alibi_slopes, scale, append, av,
@@ -1145,7 +1180,9 @@ hstu_status_t hstu_paged_layer_fwd(const hstu_shape_t* shape, const hstu_paged_c
   const size_t xbytes = (size_t)s.num_seqs * s.d_model * esize(s);
   if (overlaps(out, xbytes, X, xbytes) || overlaps(out, xbytes, workspace, w.total) ||
       overlaps(X, xbytes, workspace, w.total) || overlaps_cache(out, xbytes, *cache) ||
-      overlaps_cache(X, xbytes, *cache) || overlaps_cache(workspace, w.total, *cache))
+      overlaps_cache(X, xbytes, *cache) || overlaps_cache(workspace, w.total, *cache) ||
+      !paged_inputs_apart(s, *cache, page_table, max_pages, cache_lens, next_positions, timestamps, pos_table,
+                          time_table, alibi_slopes, out, xbytes, workspace, w.total))
     return HSTU_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((rc = run_f1(s, X, W1, b1, w.uvqk, st)) != HSTU_OK) return rc;
@@ -1183,9 +1220,13 @@ hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs
   const EvictWorkspace w = evict_layout(num_seqs, room, workspace);
   if (workspace_bytes < w.total) return HSTU_ERR_INVALID_ARG;
   const size_t lb = (size_t)num_seqs * sizeof(int64_t);
+  if (reinterpret_cast<uintptr_t>(new_lens) & 7) return HSTU_ERR_INVALID_ARG;
   if ((new_lens != cache_lens && overlaps(new_lens, lb, cache_lens, lb)) ||
-      overlaps(new_lens, lb, next_positions, lb) || overlaps(new_lens, lb, workspace, w.total) ||
-      overlaps_cache(new_lens, lb, *cache) || overlaps_cache(workspace, w.total, *cache))
+      overlaps(new_lens, lb, workspace, w.total) || overlaps_cache(new_lens, lb, *cache) ||
+      overlaps_cache(workspace, w.total, *cache) ||
+      !apart({{page_table, (size_t)(num_seqs * max_pages), 4}, {next_positions, (size_t)num_seqs, 8}}, *cache,
+             new_lens, lb, workspace, w.total) ||
+      !apart({{cache_lens, (size_t)num_seqs, 8}}, *cache, nullptr, 0, workspace, w.total))
     return HSTU_ERR_INVALID_ARG;
   paged::Evict a{};
   a.c = cache_view(*cache);

@@ -369,6 +369,9 @@ hstu_status_t hstu_candidate_layer_fwd(const hstu_shape_t* shape, const void* uv
  * The caller owns every array (naturally aligned); the struct is read during the call only.  A
  * page-table row names fewer than 2^30 slots (max_pages * page_size).
  *
+ * Tables, lengths, positions, times and offsets are naturally aligned and apart from everything that
+ * the call writes, except that new_lens may be cache_lens.
+ *
  * Sequences of one call may share pages that the call only reads: a common prefix, for
  * hstu_paged_attention_fwd on a cache without weights.  A page that is appended to, evicted from or
  * whose weights are summed belongs to one sequence, once.  Problems only the device sees are

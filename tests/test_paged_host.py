@@ -4,6 +4,8 @@ import re
 
 import pytest
 
+from tests.test_paged_abi import P, append, attend, evict, layer
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -31,3 +33,42 @@ def test_a_cluster_has_started_before_its_shared_memory_is_touched():
     assert 0 <= arrive < wait < search
     assert body.index("return;") < arrive
     assert "map_shared_rank" not in body[:wait]
+
+
+def test_what_a_call_writes_is_apart_from_its_index_arrays(hstu):
+    """The kernels read lengths, tables and biases while they write: an output, a workspace or a cache
+    array on top of one of them is refused."""
+    E = hstu.HSTU_ERR_INVALID_ARG
+    where = {"table": P(9), "lens": P(10), "nxt": P(11)}
+    for name, at in where.items():
+        assert evict(hstu, ws=at) == E, name
+        assert evict(hstu, **{name: P(5) + 64}) == E, name             # in the weights
+        assert append(hstu, **{name: P(1) + 64}) == E, name
+    assert evict(hstu, new=P(9)) == E
+    assert evict(hstu, new=P(9) + 8) == E
+    for name in ("off", "ts"):
+        assert append(hstu, **{name: P(4) + 64}) == E, name
+    where.update(now=P(8), pos=P(12), tim=P(13))
+    for name, at in where.items():
+        for call, out in ((attend, "av"), (layer, "out")):
+            assert call(hstu, **{out: at}) == E, (call, name)
+            assert call(hstu, ws=at) == E, (call, name)
+            assert call(hstu, **{name: P(2) + 64}) == E, (call, name)
+    for call, out in ((attend, "av"), (layer, "out")):
+        slopes = dict(pos=None, tim=None, ali=P(22))
+        assert call(hstu, **slopes, **{out: P(22)}) == E
+        assert call(hstu, **slopes, ws=P(22)) == E
+
+
+def test_index_arrays_are_naturally_aligned(hstu):
+    E = hstu.HSTU_ERR_INVALID_ARG
+    for call in (append, attend, layer, evict):
+        assert call(hstu, table=P(9) + 2) == E, call
+        assert call(hstu, lens=P(10) + 4) == E, call
+        assert call(hstu, nxt=P(11) + 4) == E, call
+    assert append(hstu, off=P(7) + 4) == E and append(hstu, ts=P(8) + 1) == E
+    assert evict(hstu, new=P(14) + 4) == E
+    for call in (attend, layer):
+        assert call(hstu, now=P(8) + 4) == E
+        assert call(hstu, pos=P(12) + 2) == E and call(hstu, tim=P(13) + 1) == E
+        assert call(hstu, pos=None, tim=None, ali=P(22) + 2) == E
