@@ -821,19 +821,23 @@ struct Evict {
   int64_t* new_lens;
   // workspace
   uint32_t* keys;            // [B, room]
-  uint32_t *to, *from;       // [B, moves]: slots of the pool (page * page_size + offset), or ~0: none
+  uint32_t *to, *from;       // [B, moves]: slots of the pool (page * page_size + offset)
   int64_t* count;            // [B]
   int64_t room, moves;
 };
 
-constexpr uint32_t KEY_RECENT = 0xffffffffu;
+// Keys above every weight's: of recent tokens, and of slots below the budget whose table entry is no
+// page.  Nothing can move into those, so they stay among the kept ones (there are at most `budget` of
+// them); such slots from the budget on have the lowest key and, as all below the budget come before
+// them, are never kept.
+constexpr uint32_t KEY_RECENT = 0xfffffffeu, KEY_NO_PAGE = 0xffffffffu;
 
 // The two halves of a cluster barrier; the first publishes nothing.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 
-// Keys that order tokens by what is kept first: recent ones, then by weight (sums rounded once to
-// fp32; NaN last), as unsigned integers.
+// Orders tokens by what is kept first, as unsigned integers: by weight (sums rounded once to fp32;
+// NaN last).
 __device__ __forceinline__ uint32_t weight_key(float s) {
   if (s != s) return 0u;
   s += 0.0f;                                   // -0 and +0 are equal weights
@@ -946,7 +950,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
     for (int i = 0; i < SEL_KEYS; i++) {
       const int j = start + (r0 + i) * 32;
       uint32_t k = (int64_t)pos[i] >= oldest ? KEY_RECENT : weight_key((float)sum[i]);
-      if (!(live >> i & 1)) k = 0;         // a slot of no page goes first, and nothing moves for it
+      if (!(live >> i & 1)) k = j < budget ? KEY_NO_PAGE : 0u;
       if (r0 + i < SEL_ROUNDS) s_key[(r0 + i) * SEL_THREADS] = k;
       else if (r0 + i < rounds && j < n) spill[j] = k;
     }
@@ -1155,8 +1159,8 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const Evict a
   }
   each_flagged([&](int j, uint32_t, uint32_t pg, unsigned g, unsigned m) {
     const unsigned bit = 1u << lane;
-    if ((g | m) & bit) {
-      const uint32_t flat = pg < (uint32_t)a.c.num_pages ? (pg << shift) + (j & (ps - 1)) : ~0u;
+    if ((g | m) & bit) {      // a slot that has a page: see KEY_NO_PAGE
+      const uint32_t flat = (pg << shift) + (j & (ps - 1));
       if (g & bit) a.to[b * a.moves + gap_at + __popc(g & (bit - 1u))] = flat;
       else a.from[b * a.moves + mover_at + __popc(m & (bit - 1u))] = flat;
     }
@@ -1186,7 +1190,6 @@ __global__ void __launch_bounds__(256, 8) evict_move_kernel(const Evict a, int c
     const int64_t g = x / 32, c = div_by(g, H), m = c * 32 + x % 32;
     if (m >= count) continue;
     const uint32_t h = (uint32_t)(g - c * H), to = tos[m], from = froms[m];
-    if (to == ~0u || from == ~0u) continue;
     const uint32_t rt = ((to >> shift) * H + h << shift) + (to & (ps - 1));
     const uint32_t rf = ((from >> shift) * H + h << shift) + (from & (ps - 1));
     const uint4 kr = __ldcs(k + (int64_t)rf * LPR), vr = __ldcs(v + (int64_t)rf * LPR);

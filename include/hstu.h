@@ -470,6 +470,8 @@ hstu_status_t hstu_paged_layer_fwd(const hstu_shape_t* shape, const hstu_paged_c
  * The kept tokens in slots >= budget move, in ascending order, into the slots below it that became
  * free, with K, V, position, timestamp and weights; nothing else of the cache is written, and the
  * pages from ceil(budget / page_size) on are the caller's again.
+ * A slot whose table entry is no page holds no token: below `budget` it stays one of the kept slots,
+ * from there on it is cut.
  *
  *  page_table     [num_seqs, max_pages] int32        cache_lens [num_seqs] int64
  *  next_positions [num_seqs] int64, or NULL: cache_lens

@@ -82,16 +82,23 @@ def attention(cache, uvqk, table, lens, next_positions, now, pos_table, time_tab
 
 
 def evict(cache, table, lens, next_positions, budget, recent):
-    """New lengths; the kept tokens of the slots >= budget move into the gaps below."""
+    """New lengths; the kept tokens of the slots >= budget move into the gaps below.  A length beyond the
+    table is the table's.  A slot whose entry is no page holds no token: below budget it stays one of
+    the kept slots, from there on it is cut."""
+    num_pages, ps = len(cache["k"]), cache["k"].shape[2]
     out = np.array(lens)
     for b in range(len(lens)):
-        n = int(lens[b])
+        n = min(int(lens[b]), table.shape[1] * ps)
+        out[b] = n
         if n <= budget:
             continue
         p_next = int(n if next_positions is None else next_positions[b])
         rank = []
         for j in range(n):
             p, o = _place(cache, table, b, j)
+            if not 0 <= p < num_pages:
+                rank.append((-1 if j < budget else 3, 0, 0.0, j))
+                continue
             total = 0.0
             for w in cache["weights"][p, :, o]:
                 total += float(w)

@@ -115,3 +115,56 @@ print("done")
 """
     out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and out.stdout.strip() == "done", out.stderr[-2000:]
+
+
+@pytest.mark.parametrize("lens,budget,recent,missing", [
+    ([60, 60], 30, 4, [(0, 2)]),                       # a page above the budget, and one across it
+    ([200, 60], 100, 20, [(0, 1), (0, 4), (1, 0)]),    # below it: more slots without a page than gaps
+    ([200, 150], 90, 0, [(0, 0), (0, 2), (0, 9), (0, 12), (1, 5)]),
+    ([100, 40], 30, 30, [(0, 0), (0, 1), (1, 1)]),     # only recent tokens stay: none moves for a missing page
+    ([64, 50], 16, 3, [(0, 0)]),                       # every kept slot is on the missing page
+    ([50, 200], 0, 0, [(0, 0), (1, 3)]),
+    ([70, 300], 40, 8, [(0, j) for j in range(5)])])   # a history without any page
+@pytest.mark.parametrize("entry", [-1, 1 << 30, "pages"])
+def test_evict_rows_without_a_page(hstu, lens, budget, recent, missing, entry):
+    c = Case(75, lens, 2, 64, 16, thinned=True)
+    for b, j in missing:
+        c.table[b, j] = len(c.cache["k"]) if entry == "pages" else entry
+    g = c.on_device(hstu)
+    new = hstu.hstu_cache_evict(g["cache"], g["table"], g["lens"], g["next"], budget, recent)
+    assert hstu.device_status() == hstu.HSTU_ERR_DEVICE_BAD_OFFSETS
+    assert hstu.device_status() == hstu.HSTU_OK
+    same(new, paged.evict(c.cache, c.table, c.lens, c.next, budget, recent), "new_lens")
+    check_cache(g["cache"], c.cache)          # pages of nobody included
+
+
+@pytest.mark.parametrize("aliased", [False, True])
+def test_evict_lengths_beyond_the_table(hstu, aliased):
+    # sequence 0 fills its row, sequence 1's row is the table's and its tail names no page, sequence 2
+    # is cut to what the row holds although the budget is larger
+    c = Case(76, [96, 70, 96], 2, 64, 16, extra=0)
+    c.lens[:] = [97, 1 << 50, 96]
+    for budget in (40, 96, 500):
+        d = copy.deepcopy(c)
+        g = d.on_device(hstu)
+        new = hstu.hstu_cache_evict(g["cache"], g["table"], g["lens"], g["next"], budget, 10,
+                                    new_lens=g["lens"] if aliased else None)
+        assert hstu.device_status() == hstu.HSTU_ERR_DEVICE_BAD_OFFSETS
+        # the slots behind sequence 1's tokens hold NaN weights at position -5: they go first
+        same(new, paged.evict(d.cache, d.table, d.lens, d.next, budget, 10), "new_lens")
+        check_cache(g["cache"], d.cache)
+
+
+@pytest.mark.parametrize("kind", ["random", "nan", "zero"])
+def test_evict_a_long_history_without_some_pages(hstu, kind):
+    # slots whose keys go through the workspace, and ties among the tokens that are left
+    c = Case(77, [70001] + [100] * 9, 1, 64, 1024, bias="none")
+    live = ~np.isnan(c.cache["weights"])
+    if kind != "random":
+        c.cache["weights"][live] = np.nan if kind == "nan" else 0.0
+    c.table[0, [0, 13, 40, 66, 68]] = -1
+    g = c.on_device(hstu)
+    new = hstu.hstu_cache_evict(g["cache"], g["table"], g["lens"], g["next"], 30011, 1000)
+    assert hstu.device_status() == hstu.HSTU_ERR_DEVICE_BAD_OFFSETS
+    same(new, paged.evict(c.cache, c.table, c.lens, c.next, 30011, 1000), "new_lens")
+    check_cache(g["cache"], c.cache)

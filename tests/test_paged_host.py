@@ -2,8 +2,11 @@
 import os
 import re
 
+import numpy as np
 import pytest
 
+from oracle import paged
+from tests.paged_util import Case
 from tests.test_paged_abi import P, append, attend, evict, layer
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -72,3 +75,24 @@ def test_index_arrays_are_naturally_aligned(hstu):
         assert call(hstu, now=P(8) + 4) == E
         assert call(hstu, pos=P(12) + 2) == E and call(hstu, tim=P(13) + 1) == E
         assert call(hstu, pos=None, tim=None, ali=P(22) + 2) == E
+
+
+def test_evict_without_a_page_by_hand():
+    # the row's first page is missing: its 16 slots stay, so of 20 kept slots four hold tokens.  Of slots
+    # 16..35 the most attended are 18, 35, 20 and 34: the three beyond slot 20 fill 16, 17 and 19
+    c = Case(10, [36], 1, 64, 16, bias="none")
+    c.table[0, 0] = -1
+    second, third = int(c.table[0, 1]), int(c.table[0, 2])
+    c.cache["weights"][second, 0], c.cache["weights"][third, 0, :4] = 0.0, 0.0
+    c.cache["weights"][second, 0, [2, 4, 5]] = [4.0, 2.0, 1.0]
+    c.cache["weights"][third, 0, [2, 3]] = [2.0, 3.0]
+    before = {name: c.cache[name].copy() for name in ("k", "v", "weights", "positions")}
+    assert paged.evict(c.cache, c.table, c.lens, c.next, 20, 0).tolist() == [20]
+    for name, a in before.items():
+        rows = a[second].copy() if name == "positions" else a[second].swapaxes(0, 1).copy()
+        far = a[third] if name == "positions" else a[third].swapaxes(0, 1)
+        rows[0], rows[1], rows[3] = rows[4].copy(), far[2], far[3]
+        got = c.cache[name][second] if name == "positions" else c.cache[name][second].swapaxes(0, 1)
+        assert np.array_equal(got, rows, equal_nan=True), name
+        others = [p for p in range(len(a)) if p != second]
+        assert np.array_equal(a[others], c.cache[name][others], equal_nan=True), name
