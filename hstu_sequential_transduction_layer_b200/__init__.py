@@ -325,14 +325,14 @@ class PagedCache:
     """One layer's paged key-value cache (see the C header): the caller's tensors and the struct that
     names them.  k, v [num_pages, H, page_size, hd]; positions [num_pages, page_size] int32;
     timestamps [num_pages, page_size] int64; weights [num_pages, H, page_size] fp32; the last three
-    may be None."""
+    may be None.  The tensors are written in place, never exchanged: the struct holds their
+    addresses."""
 
     def __init__(self, k, v, positions=None, timestamps=None, weights=None):
         if k.dim() != 4 or not k.is_cuda:
             raise ValueError("k is a CUDA tensor [num_pages, num_heads, page_size, head_dim]")
         pages, H, ps, hd = k.shape
-        self.k, self.v, self.positions = k, v, positions
-        self.timestamps, self.weights = timestamps, weights
+        self._tensors = k, v, positions, timestamps, weights
         self.device = k.device
         self.num_pages, self.num_heads, self.page_size, self.head_dim = pages, H, ps, hd
         n = pages * ps
@@ -343,6 +343,8 @@ class PagedCache:
             _arg("timestamps", timestamps, torch.int64, n, k.device),
             _arg("weights", weights, torch.float32, n * H, k.device))
         self.ref = ctypes.byref(self.struct)
+
+    k, v, positions, timestamps, weights = (property(lambda self, i=i: self._tensors[i]) for i in range(5))
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, num_heads: int, head_dim: int,

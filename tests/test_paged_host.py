@@ -96,3 +96,12 @@ def test_evict_without_a_page_by_hand():
         assert np.array_equal(got, rows, equal_nan=True), name
         others = [p for p in range(len(a)) if p != second]
         assert np.array_equal(a[others], c.cache[name][others], equal_nan=True), name
+
+
+def test_a_caches_tensors_are_not_exchanged(hstu):
+    # the struct that the kernels get holds their addresses: an exchanged tensor would not be seen, and
+    # the old one's memory would be written after its release
+    cache = object.__new__(hstu.PagedCache)
+    for name in ("k", "v", "positions", "timestamps", "weights"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, None)
