@@ -415,6 +415,16 @@ hstu_status_t check_table(int page_size, int64_t num_seqs, const int32_t* page_t
   return HSTU_OK;
 }
 
+// (sequence, head)s of one attention call are numbered in 31 bits
+bool pairs_fit(const hstu_shape_t& s) { return s.num_seqs < (1LL << 31) && s.num_seqs * s.num_heads < (1LL << 31); }
+constexpr int64_t kEvictMaxSeqs = 1LL << 27;   // sequences of one eviction, exclusive
+
+// A shape that the paged calls take, for their workspace sizes.
+bool paged_shape(const hstu_shape_t* s) {
+  return check_shape(s) == HSTU_OK && s->total_tokens == s->num_seqs && s->d_qk == s->d_v &&
+         paged::head_dim_supported(s->dtype, s->d_qk) && pairs_fit(*s);
+}
+
 // Checks of hstu_paged_attention_fwd's arguments (also used by the paged layer).
 hstu_status_t check_paged(const hstu_shape_t* shape, const hstu_paged_cache_t* cache,
                           const int32_t* page_table, int64_t max_pages, const int64_t* cache_lens,
@@ -429,7 +439,7 @@ hstu_status_t check_paged(const hstu_shape_t* shape, const hstu_paged_cache_t* c
   if (cache->num_heads != s.num_heads || cache->head_dim != s.d_qk || cache->head_dim != s.d_v ||
       cache->dtype != s.dtype || s.max_seq_len < 1)
     return HSTU_ERR_INVALID_ARG;
-  if (s.num_seqs * (int64_t)s.num_heads >= (1LL << 31)) return HSTU_ERR_UNSUPPORTED;
+  if (!pairs_fit(s)) return HSTU_ERR_UNSUPPORTED;
   if ((rc = check_table(cache->page_size, s.num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
   if ((rc = check_bias(shape, timestamps, pos, tim, alibi, scale)) != HSTU_OK) return rc;
   if (tim && !cache->timestamps) return HSTU_ERR_INVALID_ARG;
@@ -492,7 +502,7 @@ PagedWorkspace paged_layout(const hstu_shape_t& s, void* base) {
   w.g = b ? b + o : nullptr;
   o += align_up(T * (size_t)wv_of(s) * es);
   w.attn = b ? b + o : nullptr;
-  w.attn_bytes = hstu_paged_attention_workspace_size(&s);
+  w.attn_bytes = align_up(paged::attention_workspace_bytes(s.d_v));
   o += align_up(w.attn_bytes);
   w.total = o;
   return w;
@@ -1120,7 +1130,7 @@ hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seq
 }
 
 size_t hstu_paged_attention_workspace_size(const hstu_shape_t* shape) {
-  if (check_shape(shape) != HSTU_OK) return 0;
+  if (!paged_shape(shape)) return 0;
   return align_up(paged::attention_workspace_bytes(shape->d_v));
 }
 
@@ -1153,7 +1163,7 @@ hstu_status_t hstu_paged_attention_fwd(const hstu_shape_t* shape, const hstu_pag
 }
 
 size_t hstu_paged_layer_workspace_size(const hstu_shape_t* shape) {
-  if (check_shape(shape) != HSTU_OK) return 0;
+  if (!paged_shape(shape)) return 0;
   return paged_layout(*shape, nullptr).total;
 }
 
@@ -1197,7 +1207,8 @@ hstu_status_t hstu_paged_layer_fwd(const hstu_shape_t* shape, const hstu_paged_c
 
 size_t hstu_cache_evict_workspace_size(const hstu_paged_cache_t* cache, int64_t num_seqs,
                                        int64_t max_pages) {
-  if (check_cache(cache) != HSTU_OK || num_seqs < 0 || max_pages < 0 || max_pages >= (1LL << 31))
+  if (check_cache(cache) != HSTU_OK || num_seqs < 0 || num_seqs >= kEvictMaxSeqs || max_pages < 0 ||
+      max_pages >= (1LL << 30) / cache->page_size)
     return 0;
   return evict_layout(num_seqs, max_pages * cache->page_size, nullptr).total;
 }
@@ -1213,7 +1224,7 @@ hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs
   if (!cache->positions || !cache->weights) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_table(cache->page_size, num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
   if (num_seqs == 0) return HSTU_OK;
-  if (num_seqs >= (1LL << 27)) return HSTU_ERR_UNSUPPORTED;
+  if (num_seqs >= kEvictMaxSeqs) return HSTU_ERR_UNSUPPORTED;
   if (!new_lens || !workspace) return HSTU_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) return HSTU_ERR_INVALID_ARG;
   const int64_t room = max_pages * cache->page_size;

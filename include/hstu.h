@@ -58,7 +58,8 @@ typedef enum {
   HSTU_ERR_UNSUPPORTED = 2,    /* valid arguments outside what the kernels implement (see hstu_layer_fwd) */
   HSTU_ERR_CUDA = 3,           /* a CUDA runtime call or a kernel launch failed */
   HSTU_ERR_DEVICE_TIMEOUT = 4, /* (device status) an mbarrier wait gave up after its time limit */
-  HSTU_ERR_DEVICE_BAD_OFFSETS = 5 /* (device status) seq_offsets not monotone / not ending at T */
+  HSTU_ERR_DEVICE_BAD_OFFSETS = 5 /* (device status) seq_offsets not monotone / not ending at T; a length,
+                                     page or position that a paged cache cannot have */
 } hstu_status_t;
 
 typedef enum { HSTU_F32 = 0, HSTU_BF16 = 1 } hstu_dtype_t;
@@ -378,7 +379,8 @@ hstu_status_t hstu_candidate_layer_fwd(const hstu_shape_t* shape, const void* uv
  * reported as HSTU_ERR_DEVICE_BAD_OFFSETS: a length beyond the table or max_seq_len is clamped (its
  * new token is not stored), the tokens of an entry that is no page are left out, a position outside
  * 0 .. 2^31 - 1 is clamped.  Calls that write one cache are ordered by the caller (one stream, or
- * events).
+ * events).  A workspace size of 0, other than for no sequences, means that
+ * the call would be refused.
  */
 typedef struct {
   int64_t num_pages;

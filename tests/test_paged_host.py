@@ -1,4 +1,5 @@
 """The paged cache's host side and what can be read off its kernels' source (no GPU needed)."""
+import ctypes
 import os
 import re
 
@@ -7,7 +8,7 @@ import pytest
 
 from oracle import paged
 from tests.paged_util import Case
-from tests.test_paged_abi import P, append, attend, evict, layer
+from tests.test_paged_abi import P, append, attend, cache_of, evict, layer, shape_of
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -105,3 +106,17 @@ def test_a_caches_tensors_are_not_exchanged(hstu):
     for name in ("k", "v", "positions", "timestamps", "weights"):
         with pytest.raises(AttributeError):
             setattr(cache, name, None)
+
+
+def test_workspace_sizes_of_calls_that_are_refused(hstu):
+    """0, as for every shape that its call refuses; a wrapped product would look like a small workspace."""
+    def size(B, M, **kw):
+        return hstu.cache_evict_workspace_size(type("C", (), {"ref": ctypes.byref(cache_of(hstu, **kw))}), B, M)
+    assert size(3, 9) > 0
+    for B, M in ((1 << 27, 1), (1 << 34, 1 << 23), ((1 << 63) - 1, 1), (1, 1 << 24), (1, 1 << 31), (-1, 1), (1, -1)):
+        assert size(B, M) == 0, (B, M)
+    for f in (hstu.paged_attention_workspace_size, hstu.paged_layer_workspace_size):
+        assert f(shape_of(hstu)) > 0
+        for kw in (dict(total_tokens=4), dict(num_seqs=1 << 62), dict(num_seqs=1 << 30, total_tokens=1 << 30),
+                   dict(dtype=hstu.HSTU_F32, d_qk=96, d_v=96), dict(dtype=hstu.HSTU_F32, d_qk=64, d_v=32)):
+            assert f(shape_of(hstu, **kw)) == 0, kw
