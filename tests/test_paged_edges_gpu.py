@@ -168,3 +168,37 @@ def test_evict_a_long_history_without_some_pages(hstu, kind):
     assert hstu.device_status() == hstu.HSTU_ERR_DEVICE_BAD_OFFSETS
     same(new, paged.evict(c.cache, c.table, c.lens, c.next, 30011, 1000), "new_lens")
     check_cache(g["cache"], c.cache)
+
+
+@pytest.mark.parametrize("weights,bias", [(True, "rab"), (False, "rab"), (True, "alibi"), (False, "none")])
+@pytest.mark.parametrize("append", [True, False])
+def test_attention_without_positions_stores_the_token(hstu, weights, bias, append):
+    # slot i holds position i; with and without weights, and (ALiBi, no bias) without timestamps
+    c = Case(78, [40, 131, 0, -1], 2, 64, 16, weights=weights, positions=False, bias=bias)
+    c.next[:] = c.lens
+    g = c.on_device(hstu)
+    c.attend(hstu, g, append)                # next_positions None: the cached lengths
+    assert hstu.device_status() == hstu.HSTU_OK
+    av, want = c.want_attention(append)
+    ab, wb = c.bounds()
+    check_av(g["av"], av, ab)
+    check_cache(g["cache"], want, wb)
+
+
+@pytest.mark.parametrize("dtype,H,hd,ps,bias", [("bf16", 8, 64, 16, "rab"), ("bf16", 4, 128, 64, "alibi"),
+                                                ("fp32", 8, 32, 16, "time"), ("fp32", 2, 128, 32, "rab")])
+def test_attention_many_tiles_a_warp(hstu, dtype, H, hd, ps, bias):
+    """Eight tiles and more a warp, nearly all of one history: the producer refills stages inside a history
+    and looks ahead along it."""
+    c = Case(79, [2000 + 41 * i for i in range(25)], H, hd, ps, dtype, bias=bias, thinned=True, P=4000, Tb=32,
+             spread=40000)
+    tile = 4096 // (hd * (2 if dtype == "bf16" else 4))
+    warps = torch.cuda.get_device_properties(0).multi_processor_count * 11
+    assert H * sum(n // tile + 1 for n in c.lens.tolist()) >= 8 * warps
+    g = c.on_device(hstu)
+    av, want = c.want_attention()
+    ab, wb = c.bounds()
+    c.attend(hstu, g)
+    assert hstu.device_status() == hstu.HSTU_OK
+    check_av(g["av"], av, ab)
+    check_cache(g["cache"], want, wb)
