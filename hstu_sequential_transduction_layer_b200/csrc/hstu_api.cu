@@ -374,13 +374,33 @@ size_t cache_bytes(const hstu_paged_cache_t& c) {   // of K, and of V
   return (size_t)c.num_pages * c.page_size * c.num_heads * row_bytes(c);
 }
 
+struct CacheArrays {
+  const void* p[5];
+  size_t n[5];
+  explicit CacheArrays(const hstu_paged_cache_t& c) : p{c.k, c.v, c.positions, c.timestamps, c.weights} {
+    const size_t slots = (size_t)c.num_pages * c.page_size;
+    n[0] = n[1] = cache_bytes(c);
+    n[2] = slots * sizeof(int32_t);
+    n[3] = slots * sizeof(int64_t);
+    n[4] = slots * c.num_heads * sizeof(float);
+  }
+};
+
 // Does [p, p + n) overlap any array of the cache?
 bool overlaps_cache(const void* p, size_t n, const hstu_paged_cache_t& c) {
-  const size_t kv = cache_bytes(c), slots = (size_t)c.num_pages * c.page_size;
-  return overlaps(p, n, c.k, kv) || overlaps(p, n, c.v, kv) ||
-         overlaps(p, n, c.positions, slots * sizeof(int32_t)) ||
-         overlaps(p, n, c.timestamps, slots * sizeof(int64_t)) ||
-         overlaps(p, n, c.weights, slots * c.num_heads * sizeof(float));
+  const CacheArrays a(c);
+  for (int i = 0; i < 5; i++)
+    if (overlaps(p, n, a.p[i], a.n[i])) return true;
+  return false;
+}
+
+// Are the cache's arrays apart from each other?  K and V may be one array where they are only read.
+bool arrays_apart(const hstu_paged_cache_t& c, bool written) {
+  const CacheArrays a(c);
+  for (int i = 1; i < 5; i++)
+    for (int k = 0; k < i; k++)
+      if ((written || i != 1) && overlaps(a.p[i], a.n[i], a.p[k], a.n[k])) return false;
+  return true;
 }
 
 // An array that a call only reads: `count` elements of `size` bytes, naturally aligned; or none.
@@ -436,6 +456,7 @@ hstu_status_t check_paged(const hstu_shape_t* shape, const hstu_paged_cache_t* c
   if (s.total_tokens != s.num_seqs) return HSTU_ERR_INVALID_ARG;
   if (s.num_seqs == 0) return HSTU_OK;
   if ((rc = check_cache(cache)) != HSTU_OK) return rc;
+  if (!arrays_apart(*cache, append)) return HSTU_ERR_INVALID_ARG;
   if (cache->num_heads != s.num_heads || cache->head_dim != s.d_qk || cache->head_dim != s.d_v ||
       cache->dtype != s.dtype || s.max_seq_len < 1)
     return HSTU_ERR_INVALID_ARG;
@@ -1113,6 +1134,7 @@ hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seq
                                 const int64_t* next_positions, void* stream) {
   hstu_status_t rc = check_cache(cache);
   if (rc != HSTU_OK) return rc;
+  if (!arrays_apart(*cache, true)) return HSTU_ERR_INVALID_ARG;
   if (total_tokens < 0 || total_tokens > (1LL << 40)) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_table(cache->page_size, num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
   if (total_tokens == 0) return HSTU_OK;
@@ -1220,6 +1242,7 @@ hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs
                                size_t workspace_bytes, void* stream) {
   hstu_status_t rc = check_cache(cache);
   if (rc != HSTU_OK) return rc;
+  if (!arrays_apart(*cache, true)) return HSTU_ERR_INVALID_ARG;
   if (budget < 0 || recent < 0 || recent > budget) return HSTU_ERR_INVALID_ARG;
   if (!cache->positions || !cache->weights) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_table(cache->page_size, num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;

@@ -367,7 +367,8 @@ hstu_status_t hstu_candidate_layer_fwd(const hstu_shape_t* shape, const void* uv
  *  timestamps    [num_pages, page_size] int64 seconds, or NULL (no time table)
  *  weights       [num_pages, num_heads, page_size] fp32: sums of |a| that the token received from
  *                the tokens after it, a head; or NULL (not kept; such a cache cannot evict)
- * The caller owns every array (naturally aligned); the struct is read during the call only.  A
+ * The caller owns every array (naturally aligned, apart from the others; K and V may be one array
+ * where a call only reads them); the struct is read during the call only.  A
  * page-table row names fewer than 2^30 slots (max_pages * page_size).
  *
  * Tables, lengths, positions, times and offsets are naturally aligned and apart from everything that

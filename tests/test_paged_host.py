@@ -120,3 +120,18 @@ def test_workspace_sizes_of_calls_that_are_refused(hstu):
         for kw in (dict(total_tokens=4), dict(num_seqs=1 << 62), dict(num_seqs=1 << 30, total_tokens=1 << 30),
                    dict(dtype=hstu.HSTU_F32, d_qk=96, d_v=96), dict(dtype=hstu.HSTU_F32, d_qk=64, d_v=32)):
             assert f(shape_of(hstu, **kw)) == 0, kw
+
+
+def test_a_caches_arrays_are_apart(hstu):
+    """Positions on top of times, weights on top of keys and the like are refused; K and V may be one
+    array where they are only read."""
+    E = hstu.HSTU_ERR_INVALID_ARG
+    slots, kv = 100 * 64, 100 * 64 * 2 * 64 * 2
+    for call in (append, attend, layer, evict):
+        for over in (dict(v=P(1) + kv - 16), dict(v=P(1)), dict(positions=P(1) + 4), dict(positions=P(2) + kv - 4),
+                     dict(timestamps=P(3) + 4 * slots - 8), dict(weights=P(4) + 8 * slots - 4), dict(weights=P(1)),
+                     dict(weights=P(3)), dict(positions=P(5) + 8 * slots - 4)):
+            assert call(hstu, cache=cache_of(hstu, **over)) == E, (call, over)
+    assert attend(hstu, cache=cache_of(hstu, v=P(1)), append=0) != E
+    assert attend(hstu, cache=cache_of(hstu, weights=P(1)), append=0) == E
+    assert append(hstu, cache=cache_of(hstu, v=P(1) + kv, k=P(1)), T=0) == hstu.HSTU_OK      # side by side
