@@ -1318,10 +1318,11 @@ inline bool wide_clusters_fit() {
 }
 
 inline hstu_status_t launch_evict(const Evict& a, int row_bytes, int sms, cudaStream_t st) {
-  // As many CTAs as hold the keys of a row's slots, and more while there are SMs for them, up to 8.
-  // Above 4096 slots a CTA of eight, 16 for few sequences: one history of 32 771 slots 28.4 us (with
-  // eight 33.7), six 62 (67), but eight of 60 000 101 (96): not all fit the GPU at once; and 16 000
-  // slots 23.9 (21.8).
+  // As many CTAs as hold the keys of a row's slots, and more while there are SMs for them, up to 8
+  // (8192 slots 15.2 us an eviction, with four 16.2; 16 384 17.0, 20.0).  Rows of more slots than eight
+  // CTAs score in one go get 16 for a few sequences: below that their wider barriers cost more (24 576
+  // slots 19.2 us, with eight 18.9; 28 672 19.7, 19.9; 32 768 20.1, 20.8; 40 960 21.0, 25.8; 100 000 28.3,
+  // 46.8, one history as six).  Seven such clusters fit the GPU at once, an eighth waits (32 768 slots 38).
   int S = 1;
   while (S < 8 && ((int64_t)S * SEL_THREADS * SEL_ROUNDS < a.room || 2 * S * a.B <= sms)) S *= 2;
   if (!succeeded(cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_SMEM)))
