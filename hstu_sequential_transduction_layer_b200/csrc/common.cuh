@@ -21,6 +21,14 @@ __device__ __forceinline__ void report(int code) { atomicCAS(&g_device_status, 0
 inline std::atomic<uint64_t> g_launches{0};
 inline void count_launch(uint64_t n = 1) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
+// Whether a runtime call succeeded.  A failed call's error is taken back, so that no later check of
+// the last error meets it; an error that some earlier call left is neither looked at nor touched.
+inline bool succeeded(cudaError_t e) {
+  if (e == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 using bf16 = __nv_bfloat16;
 
 template <typename T> struct io;

@@ -61,7 +61,7 @@ CtxGetCurrentFn ctx_get_current_fn() {
   static CtxGetCurrentFn fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
+    if (succeeded(cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q)) &&
         q == cudaDriverEntryPointSuccess)
       return reinterpret_cast<CtxGetCurrentFn>(p);
     return static_cast<CtxGetCurrentFn>(nullptr);
@@ -83,11 +83,11 @@ ScratchAddr g_noalloc_addr[kMaxDevices] = {};
 // once per device and context (the first call there, and again after the context was replaced).
 hstu_status_t noalloc_scratch(void** out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return HSTU_ERR_CUDA;
+  if (!succeeded(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return HSTU_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_noalloc_mutex);
   auto lookup = [](void** p) {
-    return cudaGetSymbolAddress(p, g_noalloc_scratch) == cudaSuccess && *p ? HSTU_OK
-                                                                           : HSTU_ERR_CUDA;
+    return succeeded(cudaGetSymbolAddress(p, g_noalloc_scratch)) && *p ? HSTU_OK
+                                                                      : HSTU_ERR_CUDA;
   };
   const void* ctx = current_context();
   if (!ctx) {  // nothing current yet: a runtime call makes the device's primary context current
@@ -704,11 +704,11 @@ const char* hstu_status_string(hstu_status_t st) {
 }
 
 hstu_status_t hstu_get_device_status(void* stream) {
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (!succeeded(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)))) return HSTU_ERR_CUDA;
   int v = 0;
-  if (cudaMemcpyFromSymbol(&v, hstu::g_device_status, sizeof(int)) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (!succeeded(cudaMemcpyFromSymbol(&v, hstu::g_device_status, sizeof(int)))) return HSTU_ERR_CUDA;
   const int zero = 0;
-  if (cudaMemcpyToSymbol(hstu::g_device_status, &zero, sizeof(int)) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (!succeeded(cudaMemcpyToSymbol(hstu::g_device_status, &zero, sizeof(int)))) return HSTU_ERR_CUDA;
   return static_cast<hstu_status_t>(v);
 }
 
@@ -1063,7 +1063,7 @@ hstu_status_t hstu_layer_bwd(const hstu_shape_t* shape, const void* X, const int
     auto go = [&](auto nc) {
       auto kern = bwd::ln_gate_bwd_reg_kernel<decltype(nc)::value>;
       int per_sm = 1;
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 256, 0) != cudaSuccess ||
+      if (!succeeded(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 256, 0)) ||
           per_sm < 1)
         per_sm = 1;
       const int64_t full = (int64_t)per_sm * tc::num_sms();   // one wave of resident blocks
@@ -1085,8 +1085,8 @@ hstu_status_t hstu_layer_bwd(const hstu_shape_t* shape, const void* X, const int
     const int64_t blocks = T < 4LL * tc::num_sms() * 8 ? (T + 7) / 8 : 4LL * tc::num_sms();
     const size_t smem = (size_t)2 * wv * sizeof(float);
     if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(bwd::ln_gate_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
+        !succeeded(cudaFuncSetAttribute(bwd::ln_gate_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)smem)))
       return HSTU_ERR_CUDA;
     bwd::ln_gate_bwd_kernel<<<(unsigned)blocks, 256, smem, st>>>(
         T, (int)wv, n1, (const float*)fw.av, (const bf16*)fw.uvqk, (const float*)w.dg,
@@ -1440,19 +1440,19 @@ hstu_status_t hstu_layer_pipeline_create(const hstu_shape_t* capacity, int32_t d
   p->depth = depth;
   const size_t T = (size_t)capacity->total_tokens, B = (size_t)capacity->num_seqs;
   const size_t xb = T * (size_t)capacity->d_model * esize(*capacity);
-  bool okc = cudaStreamCreateWithFlags(&p->s_in, cudaStreamNonBlocking) == cudaSuccess &&
-             cudaStreamCreateWithFlags(&p->s_comp, cudaStreamNonBlocking) == cudaSuccess &&
-             cudaStreamCreateWithFlags(&p->s_out, cudaStreamNonBlocking) == cudaSuccess &&
-             cudaEventCreate(&p->t0) == cudaSuccess && cudaEventCreate(&p->t1) == cudaSuccess;
+  bool okc = succeeded(cudaStreamCreateWithFlags(&p->s_in, cudaStreamNonBlocking)) &&
+             succeeded(cudaStreamCreateWithFlags(&p->s_comp, cudaStreamNonBlocking)) &&
+             succeeded(cudaStreamCreateWithFlags(&p->s_out, cudaStreamNonBlocking)) &&
+             succeeded(cudaEventCreate(&p->t0)) && succeeded(cudaEventCreate(&p->t1));
   for (int i = 0; okc && i < depth; i++) {
     void *x = nullptr, *o = nullptr;
     int64_t *f = nullptr, *tt = nullptr;
     cudaEvent_t e[3] = {nullptr, nullptr, nullptr};
-    okc = cudaMalloc(&x, xb) == cudaSuccess && cudaMalloc(&o, xb) == cudaSuccess &&
-          cudaMalloc(&f, (B + 1) * sizeof(int64_t)) == cudaSuccess &&
-          cudaMalloc(&tt, T * sizeof(int64_t)) == cudaSuccess;
+    okc = succeeded(cudaMalloc(&x, xb)) && succeeded(cudaMalloc(&o, xb)) &&
+          succeeded(cudaMalloc(&f, (B + 1) * sizeof(int64_t))) &&
+          succeeded(cudaMalloc(&tt, T * sizeof(int64_t)));
     for (int k = 0; okc && k < 3; k++)
-      okc = cudaEventCreateWithFlags(&e[k], cudaEventDisableTiming) == cudaSuccess;
+      okc = succeeded(cudaEventCreateWithFlags(&e[k], cudaEventDisableTiming));
     p->X.push_back(x);
     p->out.push_back(o);
     p->off.push_back(f);
@@ -1463,7 +1463,7 @@ hstu_status_t hstu_layer_pipeline_create(const hstu_shape_t* capacity, int32_t d
   }
   if (okc) {
     p->ws_bytes = hstu_layer_fwd_workspace_size(capacity);
-    okc = p->ws_bytes > 0 && cudaMalloc(&p->ws, p->ws_bytes) == cudaSuccess;
+    okc = p->ws_bytes > 0 && succeeded(cudaMalloc(&p->ws, p->ws_bytes));
   }
   if (!okc) {
     cudaGetLastError();
@@ -1504,26 +1504,26 @@ hstu_status_t hstu_layer_pipeline_submit(hstu_layer_pipeline_t* p, const hstu_sh
   const bool reuse = p->count >= (uint64_t)p->depth;
   bool okc = true;
   // copy in: the slot's inputs are free once the layer that last read them has finished
-  if (reuse) okc = cudaStreamWaitEvent(p->s_in, p->comp_done[slot], 0) == cudaSuccess;
-  okc = okc && cudaMemcpyAsync(p->X[slot], X_host, xb, cudaMemcpyHostToDevice, p->s_in) == cudaSuccess;
-  okc = okc && cudaMemcpyAsync(p->off[slot], seq_offsets_host, (size_t)(s.num_seqs + 1) * sizeof(int64_t),
-                               cudaMemcpyHostToDevice, p->s_in) == cudaSuccess;
+  if (reuse) okc = succeeded(cudaStreamWaitEvent(p->s_in, p->comp_done[slot], 0));
+  okc = okc && succeeded(cudaMemcpyAsync(p->X[slot], X_host, xb, cudaMemcpyHostToDevice, p->s_in));
+  okc = okc && succeeded(cudaMemcpyAsync(p->off[slot], seq_offsets_host, (size_t)(s.num_seqs + 1) * sizeof(int64_t),
+                                         cudaMemcpyHostToDevice, p->s_in));
   if (time_table)
-    okc = okc && cudaMemcpyAsync(p->ts[slot], timestamps_host, (size_t)s.total_tokens * sizeof(int64_t),
-                                 cudaMemcpyHostToDevice, p->s_in) == cudaSuccess;
-  okc = okc && cudaEventRecord(p->in_done[slot], p->s_in) == cudaSuccess;
+    okc = okc && succeeded(cudaMemcpyAsync(p->ts[slot], timestamps_host, (size_t)s.total_tokens * sizeof(int64_t),
+                                           cudaMemcpyHostToDevice, p->s_in));
+  okc = okc && succeeded(cudaEventRecord(p->in_done[slot], p->s_in));
   // compute: after the copy in, and after the slot's previous output has been read back
-  okc = okc && cudaStreamWaitEvent(p->s_comp, p->in_done[slot], 0) == cudaSuccess;
-  if (reuse) okc = okc && cudaStreamWaitEvent(p->s_comp, p->out_done[slot], 0) == cudaSuccess;
+  okc = okc && succeeded(cudaStreamWaitEvent(p->s_comp, p->in_done[slot], 0));
+  if (reuse) okc = okc && succeeded(cudaStreamWaitEvent(p->s_comp, p->out_done[slot], 0));
   if (!okc) return HSTU_ERR_CUDA;
   rc = hstu_layer_fwd(shape, p->X[slot], p->off[slot], time_table ? p->ts[slot] : nullptr, W1, b1,
                       W2, b2, ln_w, ln_b, pos_table, time_table, alibi_slopes, scale,
                       p->out[slot], p->ws, p->ws_bytes, p->s_comp);
   if (rc != HSTU_OK) return rc;
-  okc = cudaEventRecord(p->comp_done[slot], p->s_comp) == cudaSuccess &&
-        cudaStreamWaitEvent(p->s_out, p->comp_done[slot], 0) == cudaSuccess &&
-        cudaMemcpyAsync(out_host, p->out[slot], xb, cudaMemcpyDeviceToHost, p->s_out) == cudaSuccess &&
-        cudaEventRecord(p->out_done[slot], p->s_out) == cudaSuccess;
+  okc = succeeded(cudaEventRecord(p->comp_done[slot], p->s_comp)) &&
+        succeeded(cudaStreamWaitEvent(p->s_out, p->comp_done[slot], 0)) &&
+        succeeded(cudaMemcpyAsync(out_host, p->out[slot], xb, cudaMemcpyDeviceToHost, p->s_out)) &&
+        succeeded(cudaEventRecord(p->out_done[slot], p->s_out));
   if (!okc) return HSTU_ERR_CUDA;
   p->count++;
   return HSTU_OK;
@@ -1532,22 +1532,22 @@ hstu_status_t hstu_layer_pipeline_submit(hstu_layer_pipeline_t* p, const hstu_sh
 hstu_status_t hstu_layer_pipeline_sync(hstu_layer_pipeline_t* p) {
   if (!p) return HSTU_ERR_INVALID_ARG;
   for (cudaStream_t s : {p->s_in, p->s_comp, p->s_out})
-    if (cudaStreamSynchronize(s) != cudaSuccess) return HSTU_ERR_CUDA;
+    if (!succeeded(cudaStreamSynchronize(s))) return HSTU_ERR_CUDA;
   return HSTU_OK;
 }
 
 hstu_status_t hstu_layer_pipeline_timing_begin(hstu_layer_pipeline_t* p) {
   if (!p) return HSTU_ERR_INVALID_ARG;
   p->timing = true;
-  return cudaEventRecord(p->t0, p->s_in) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  return succeeded(cudaEventRecord(p->t0, p->s_in)) ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
 hstu_status_t hstu_layer_pipeline_timing_end(hstu_layer_pipeline_t* p, float* ms) {
   if (!p || !ms || !p->timing) return HSTU_ERR_INVALID_ARG;
   p->timing = false;
-  if (cudaEventRecord(p->t1, p->s_out) != cudaSuccess || hstu_layer_pipeline_sync(p) != HSTU_OK)
+  if (!succeeded(cudaEventRecord(p->t1, p->s_out)) || hstu_layer_pipeline_sync(p) != HSTU_OK)
     return HSTU_ERR_CUDA;
-  return cudaEventElapsedTime(ms, p->t0, p->t1) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  return succeeded(cudaEventElapsedTime(ms, p->t0, p->t1)) ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
 void hstu_layer_pipeline_destroy(hstu_layer_pipeline_t* p) { pipeline_free(p); }

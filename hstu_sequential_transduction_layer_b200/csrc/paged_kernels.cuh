@@ -1209,14 +1209,6 @@ __global__ void __launch_bounds__(256, 8) evict_move_kernel(const Evict a, int c
 // Launchers (arguments already checked)
 // ------------------------------------------------------------------------------------------------
 
-// Whether a runtime call succeeded.  A failed call's error is taken back, so that no later check of
-// the last error meets it; an error that some earlier call left is neither looked at nor touched.
-inline bool succeeded(cudaError_t e) {
-  if (e == cudaSuccess) return true;
-  cudaGetLastError();
-  return false;
-}
-
 // Launches a kernel of this file (see after_previous), `cluster` CTAs a cluster.
 template <typename... P, typename... A>
 hstu_status_t launch(void (*kern)(P...), int64_t grid, int threads, int smem, int cluster, cudaStream_t st,

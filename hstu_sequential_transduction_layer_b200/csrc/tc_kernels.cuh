@@ -21,7 +21,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   std::call_once(once, [] {
     cudaDriverEntryPointQueryResult q;
     void* p = nullptr;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+    if (succeeded(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q)) &&
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
@@ -101,8 +101,7 @@ hstu_status_t launch_gemm_cfg(int64_t M, int N, int K, const bf16* A, const bf16
   }
   auto kern = gemm_tc_kernel<BN, EPI, RX>;
   // set on every launch: the attribute is per device and the call is cheap
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) !=
-      cudaSuccess)
+  if (!succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM)))
     return HSTU_ERR_CUDA;
   // every split gets at least one K block
   const int kblocks = K / Cfg::BK;
@@ -147,7 +146,7 @@ hstu_status_t launch_ln_f2_n(int64_t M, int n1, const float* av, const bf16* uvq
   if (!make_map_bf16(&tx, X, N, M, N, 64, 128)) return HSTU_ERR_CUDA;
   auto kern = ln_f2_kernel<N, N>;
   constexpr int smem = Cfg::SMEM + 1024;   // + alignment slack
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  if (!succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
     return HSTU_ERR_CUDA;
   const int64_t blocks = (M + Cfg::BM - 1) / Cfg::BM;
   const int grid = (int)(blocks < num_sms() ? blocks : num_sms());
@@ -239,8 +238,7 @@ hstu_status_t launch_attention_kernel(const CUtensorMap& tm, const CUtensorMap& 
                                       cudaStream_t st) {
   using Cfg = AttnCfg<HD>;
   auto kern = attention_tc_kernel<HD, BIAS, CAND>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM) !=
-      cudaSuccess)
+  if (!succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM)))
     return HSTU_ERR_CUDA;
   kern<<<grid, ATT_THREADS, Cfg::SMEM, st>>>(tm, tmq, prm, sch);
   count_launch();
@@ -270,8 +268,8 @@ inline hstu_status_t launch_attention(int64_t T, int64_t B, int H, int hd, int64
   const int64_t gb64 = (32LL << 20) / kv_bytes_per_group;
   const int gb = !dynamic ? (1 << 30) : (int)(gb64 < 1 ? 1 : (gb64 > 256 ? 256 : gb64));
   if (sched_smem > 48 * 1024 &&
-      cudaFuncSetAttribute(attn_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sched_smem) != cudaSuccess)
+      !succeeded(cudaFuncSetAttribute(attn_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)sched_smem)))
     return HSTU_ERR_CUDA;
   const int64_t capacity = attention_capacity(T, B, H);
   attn_schedule_kernel<<<1, 1024, sched_smem, st>>>(off, B, T, H, max_pairs, gb, capacity, sch);
@@ -327,8 +325,7 @@ hstu_status_t launch_attention_bwd_kernel(const CUtensorMap& tm, const CUtensorM
                                           const CUtensorMap& tdq, const BwdParams& prm,
                                           const AttnSchedule& sch, int grid, cudaStream_t st) {
   auto kern = attention_bwd_kernel<BM, HD>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdCfg<HD>::SMEM) !=
-      cudaSuccess)
+  if (!succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdCfg<HD>::SMEM)))
     return HSTU_ERR_CUDA;
   kern<<<grid, BWD_THREADS, BwdCfg<HD>::SMEM, st>>>(tm, tdo, tdq, prm, sch);
   count_launch();
@@ -336,8 +333,8 @@ hstu_status_t launch_attention_bwd_kernel(const CUtensorMap& tm, const CUtensorM
   if constexpr (!BwdCfg<HD>::DQ) {
     // dQ from the query-stationary kernel, on the same schedule
     auto dqk = attention_bwd_dq_kernel<BM, HD>;
-    if (cudaFuncSetAttribute(dqk, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             BwdDqCfg<HD>::SMEM) != cudaSuccess)
+    if (!succeeded(cudaFuncSetAttribute(dqk, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        BwdDqCfg<HD>::SMEM)))
       return HSTU_ERR_CUDA;
     dqk<<<grid, BWD_THREADS, BwdDqCfg<HD>::SMEM, st>>>(tm, tdo, prm, sch);
     count_launch();
@@ -380,8 +377,8 @@ inline hstu_status_t launch_attention_bwd(int64_t T, int64_t B, int H, int hd, i
   const AttnSchedule sch = attention_schedule_view(ws, B);
   const size_t sched_smem = 2 * (size_t)(max_tiles + 2) * sizeof(unsigned long long);
   if (sched_smem > 48 * 1024 &&
-      cudaFuncSetAttribute(bwd_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sched_smem) != cudaSuccess)
+      !succeeded(cudaFuncSetAttribute(bwd_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)sched_smem)))
     return HSTU_ERR_CUDA;
   const int64_t capacity = attention_bwd_capacity(T, B, H);
   bwd_schedule_kernel<<<1, 1024, sched_smem, st>>>(off, B, T, H, max_tiles, capacity, sch);
@@ -449,8 +446,8 @@ inline hstu_status_t launch_candidate_attention(
   sch.items = reinterpret_cast<int64_t*>(b + 256 + ((32 * B + 255) / 256) * 256);
   const size_t sched_smem = 2 * (size_t)(max_tiles + 1) * sizeof(unsigned long long);
   if (sched_smem > 48 * 1024 &&
-      cudaFuncSetAttribute(cand_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sched_smem) != cudaSuccess)
+      !succeeded(cudaFuncSetAttribute(cand_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)sched_smem)))
     return HSTU_ERR_CUDA;
   const int64_t capacity = candidate_capacity(Tc, B, H);
   cand_schedule_kernel<<<1, 1024, sched_smem, st>>>(hoff, coff, B, Th, Tc, H, max_tiles, capacity,

@@ -45,8 +45,8 @@ def test_evict_behind_other_work(hstu, lens, ps, budget):
 
 
 def leave_an_error(hstu):
-    """Leaves a CUDA error of an earlier call behind in the library's runtime: its status is asked for
-    on a stream that is being captured, which CUDA refuses (and the capture is given up)."""
+    """A CUDA call of the library's that fails, as may any before the call that is tested: its status is
+    asked for on a stream that is being captured, which CUDA refuses (and the capture is given up)."""
     cuda, graph = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p()
     st = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -202,3 +202,22 @@ def test_attention_many_tiles_a_warp(hstu, dtype, H, hd, ps, bias):
     assert hstu.device_status() == hstu.HSTU_OK
     check_av(g["av"], av, ab)
     check_cache(g["cache"], want, wb)
+
+
+def test_layer_behind_an_earlier_error(hstu):
+    H, hd, B = 2, 32, 3
+    c = Case(80, [20, 5, 0], H, hd, 16, "fp32", bias="none")
+    w = {k: c.dev(0.1 * c.rng.standard_normal(s), torch.float32)
+         for k, s in (("W1", (64, 256)), ("b1", 256), ("W2", (64, 64)), ("b2", 64), ("ln_w", 64), ("ln_b", 64))}
+    X = c.dev(values(c.rng, (B, 64), "fp32"), torch.float32)
+    out = []
+    for behind in (False, True):
+        g = c.on_device(hstu)
+        if behind:
+            leave_an_error(hstu)
+        out.append(hstu.hstu_paged_layer_fwd(g["shape"], g["cache"], X, g["table"], g["lens"], g["next"], None,
+                                             w["W1"], w["b1"], w["W2"], w["b2"], w["ln_w"], w["ln_b"], None, None,
+                                             None, c.scale))
+        assert hstu.device_status() == hstu.HSTU_OK
+        out.append(g["cache"].k.nan_to_num(7.0))
+    assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
