@@ -333,7 +333,7 @@ class PagedCache:
             raise ValueError("k is a CUDA tensor [num_pages, num_heads, page_size, head_dim]")
         pages, H, ps, hd = k.shape
         self._tensors = k, v, positions, timestamps, weights
-        self.device = k.device
+        self.device, self.dtype = k.device, k.dtype
         self.num_pages, self.num_heads, self.page_size, self.head_dim = pages, H, ps, hd
         n = pages * ps
         self.struct = HstuPagedCache(
@@ -432,7 +432,7 @@ def hstu_cache_append(cache: PagedCache, uvqk, seq_offsets, timestamps, page_tab
     T, i64 = int(uvqk.shape[0]), torch.int64
     _call(_lib.hstu_cache_append, "hstu_cache_append", cache.device, stream, cache.ref, B, T,
           *_args(cache.device, (
-              ("uvqk", uvqk, cache.k.dtype, T * 4 * cache.num_heads * cache.head_dim),
+              ("uvqk", uvqk, cache.dtype, T * 4 * cache.num_heads * cache.head_dim),
               ("seq_offsets", seq_offsets, i64, B + 1), ("timestamps", timestamps, i64, T),
               ("page_table", page_table, torch.int32, B * M))), M,
           *_args(cache.device, (("cache_lens", cache_lens, i64, B),
@@ -454,7 +454,7 @@ def hstu_paged_attention_fwd(shape: HstuShape, cache: PagedCache, uvqk, page_tab
         raise ValueError(f"page_table has {B} rows, the shape {shape.num_seqs} sequences")
     H = shape.num_heads
     up, tp, lp, np_, sp, pos, tim, ali, ap = _args(dev, (
-        ("uvqk", uvqk, cache.k.dtype, B * 4 * w), ("page_table", page_table, torch.int32, B * M),
+        ("uvqk", uvqk, cache.dtype, B * 4 * w), ("page_table", page_table, torch.int32, B * M),
         ("cache_lens", cache_lens, i64, B), ("next_positions", next_positions, i64, B),
         ("timestamps", timestamps, i64, B), ("pos_table", pos_table, f32, H * shape.n_pos_buckets),
         ("time_table", time_table, f32, H * shape.n_time_buckets),
@@ -476,7 +476,7 @@ def hstu_paged_layer_fwd(shape: HstuShape, cache: PagedCache, X, page_table, cac
                          workspace=None, stream=None):
     """One HSTU layer over one new token a sequence, against the layer's paged cache."""
     B, M = _rows(page_table)
-    w, d, dt, dev = cache.num_heads * cache.head_dim, shape.d_model, cache.k.dtype, cache.device
+    w, d, dt, dev = cache.num_heads * cache.head_dim, shape.d_model, cache.dtype, cache.device
     if shape.num_seqs != B:
         raise ValueError(f"page_table has {B} rows, the shape {shape.num_seqs} sequences")
     if out is None:

@@ -387,32 +387,31 @@ struct CacheArrays {
 };
 
 // Does [p, p + n) overlap any array of the cache?
-bool overlaps_cache(const void* p, size_t n, const hstu_paged_cache_t& c) {
-  const CacheArrays a(c);
+bool overlaps_cache(const void* p, size_t n, const CacheArrays& a) {
   for (int i = 0; i < 5; i++)
     if (overlaps(p, n, a.p[i], a.n[i])) return true;
   return false;
 }
 
 // Are the cache's arrays apart from each other?  K and V may be one array where they are only read.
-bool arrays_apart(const hstu_paged_cache_t& c, bool written) {
-  const CacheArrays a(c);
+bool arrays_apart(const CacheArrays& a, bool written) {
   for (int i = 1; i < 5; i++)
     for (int k = 0; k < i; k++)
       if ((written || i != 1) && overlaps(a.p[i], a.n[i], a.p[k], a.n[k])) return false;
   return true;
 }
 
-// An array that a call only reads: `count` elements of `size` bytes, naturally aligned; or none.
+// An array that a call only reads: `count` elements of `size` bytes (a power of two), naturally
+// aligned; or none.
 struct ReadOnly {
   const void* p;
   size_t count, size;
-  bool aligned() const { return reinterpret_cast<uintptr_t>(p) % size == 0; }
+  bool aligned() const { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
   bool meets(const void* q, size_t n) const { return overlaps(q, n, p, count * size); }
 };
 
 // Are the arrays aligned, and apart from the cache and from the two ranges that a call writes?
-bool apart(std::initializer_list<ReadOnly> arrays, const hstu_paged_cache_t& c, const void* out = nullptr,
+bool apart(std::initializer_list<ReadOnly> arrays, const CacheArrays& c, const void* out = nullptr,
            size_t out_bytes = 0, const void* ws = nullptr, size_t ws_bytes = 0) {
   for (const ReadOnly& a : arrays)
     if (!a.aligned() || a.meets(out, out_bytes) || a.meets(ws, ws_bytes) || overlaps_cache(a.p, a.count * a.size, c))
@@ -456,7 +455,7 @@ hstu_status_t check_paged(const hstu_shape_t* shape, const hstu_paged_cache_t* c
   if (s.total_tokens != s.num_seqs) return HSTU_ERR_INVALID_ARG;
   if (s.num_seqs == 0) return HSTU_OK;
   if ((rc = check_cache(cache)) != HSTU_OK) return rc;
-  if (!arrays_apart(*cache, append)) return HSTU_ERR_INVALID_ARG;
+  if (!arrays_apart(CacheArrays(*cache), append)) return HSTU_ERR_INVALID_ARG;
   if (cache->num_heads != s.num_heads || cache->head_dim != s.d_qk || cache->head_dim != s.d_v ||
       cache->dtype != s.dtype || s.max_seq_len < 1)
     return HSTU_ERR_INVALID_ARG;
@@ -496,7 +495,7 @@ hstu_status_t run_paged_attention(const hstu_shape_t& s, const hstu_paged_cache_
 }
 
 // The same for what the attention reads besides U|V|Q|K and the cache.
-bool paged_inputs_apart(const hstu_shape_t& s, const hstu_paged_cache_t& cache, const int32_t* page_table,
+bool paged_inputs_apart(const hstu_shape_t& s, const CacheArrays& cache, const int32_t* page_table,
                         int64_t max_pages, const int64_t* cache_lens, const int64_t* next_positions,
                         const int64_t* timestamps, const float* pos, const float* tim, const float* alibi,
                         const void* out, size_t out_bytes, const void* ws, size_t ws_bytes) {
@@ -1134,17 +1133,18 @@ hstu_status_t hstu_cache_append(const hstu_paged_cache_t* cache, int64_t num_seq
                                 const int64_t* next_positions, void* stream) {
   hstu_status_t rc = check_cache(cache);
   if (rc != HSTU_OK) return rc;
-  if (!arrays_apart(*cache, true)) return HSTU_ERR_INVALID_ARG;
+  const CacheArrays arrays(*cache);
+  if (!arrays_apart(arrays, true)) return HSTU_ERR_INVALID_ARG;
   if (total_tokens < 0 || total_tokens > (1LL << 40)) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_table(cache->page_size, num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
   if (total_tokens == 0) return HSTU_OK;
   if (num_seqs == 0 || !uvqk || !seq_offsets || !aligned16(uvqk)) return HSTU_ERR_INVALID_ARG;
   if (cache->timestamps && !timestamps) return HSTU_ERR_INVALID_ARG;
   const size_t B = (size_t)num_seqs, T = (size_t)total_tokens;
-  if (overlaps_cache(uvqk, T * 4 * cache->num_heads * row_bytes(*cache), *cache) ||
+  if (overlaps_cache(uvqk, T * 4 * cache->num_heads * row_bytes(*cache), arrays) ||
       !apart({{seq_offsets, B + 1, 8}, {timestamps, T, 8}, {page_table, B * max_pages, 4}, {cache_lens, B, 8},
               {next_positions, B, 8}},
-             *cache))
+             arrays))
     return HSTU_ERR_INVALID_ARG;
   return paged::launch_append(cache_view(*cache), row_bytes(*cache), total_tokens, num_seqs, uvqk,
                               seq_offsets, timestamps, page_table, max_pages, cache_lens,
@@ -1172,11 +1172,12 @@ hstu_status_t hstu_paged_attention_fwd(const hstu_shape_t* shape, const hstu_pag
   if (!aligned16(uvqk) || !aligned16(av)) return HSTU_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) return HSTU_ERR_INVALID_ARG;
   if (workspace_bytes < hstu_paged_attention_workspace_size(shape)) return HSTU_ERR_INVALID_ARG;
+  const CacheArrays arrays(*cache);
   const size_t avb = (size_t)s.num_seqs * wv_of(s) * 4, ub = (size_t)s.num_seqs * n1_of(s) * esize(s);
   if (overlaps(av, avb, uvqk, ub) || overlaps(av, avb, workspace, workspace_bytes) ||
-      overlaps(uvqk, ub, workspace, workspace_bytes) || overlaps_cache(av, avb, *cache) ||
-      overlaps_cache(uvqk, ub, *cache) || overlaps_cache(workspace, workspace_bytes, *cache) ||
-      !paged_inputs_apart(s, *cache, page_table, max_pages, cache_lens, next_positions, timestamps, pos_table,
+      overlaps(uvqk, ub, workspace, workspace_bytes) || overlaps_cache(av, avb, arrays) ||
+      overlaps_cache(uvqk, ub, arrays) || overlaps_cache(workspace, workspace_bytes, arrays) ||
+      !paged_inputs_apart(s, arrays, page_table, max_pages, cache_lens, next_positions, timestamps, pos_table,
                           time_table, alibi_slopes, av, avb, workspace, workspace_bytes))
     return HSTU_ERR_INVALID_ARG;
   return run_paged_attention(s, *cache, uvqk, page_table, max_pages, cache_lens, next_positions,
@@ -1209,11 +1210,12 @@ hstu_status_t hstu_paged_layer_fwd(const hstu_shape_t* shape, const hstu_paged_c
   if (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) return HSTU_ERR_INVALID_ARG;
   const PagedWorkspace w = paged_layout(s, workspace);
   if (workspace_bytes < w.total) return HSTU_ERR_INVALID_ARG;
+  const CacheArrays arrays(*cache);
   const size_t xbytes = (size_t)s.num_seqs * s.d_model * esize(s);
   if (overlaps(out, xbytes, X, xbytes) || overlaps(out, xbytes, workspace, w.total) ||
-      overlaps(X, xbytes, workspace, w.total) || overlaps_cache(out, xbytes, *cache) ||
-      overlaps_cache(X, xbytes, *cache) || overlaps_cache(workspace, w.total, *cache) ||
-      !paged_inputs_apart(s, *cache, page_table, max_pages, cache_lens, next_positions, timestamps, pos_table,
+      overlaps(X, xbytes, workspace, w.total) || overlaps_cache(out, xbytes, arrays) ||
+      overlaps_cache(X, xbytes, arrays) || overlaps_cache(workspace, w.total, arrays) ||
+      !paged_inputs_apart(s, arrays, page_table, max_pages, cache_lens, next_positions, timestamps, pos_table,
                           time_table, alibi_slopes, out, xbytes, workspace, w.total))
     return HSTU_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1242,7 +1244,8 @@ hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs
                                size_t workspace_bytes, void* stream) {
   hstu_status_t rc = check_cache(cache);
   if (rc != HSTU_OK) return rc;
-  if (!arrays_apart(*cache, true)) return HSTU_ERR_INVALID_ARG;
+  const CacheArrays arrays(*cache);
+  if (!arrays_apart(arrays, true)) return HSTU_ERR_INVALID_ARG;
   if (budget < 0 || recent < 0 || recent > budget) return HSTU_ERR_INVALID_ARG;
   if (!cache->positions || !cache->weights) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_table(cache->page_size, num_seqs, page_table, max_pages, cache_lens)) != HSTU_OK) return rc;
@@ -1256,11 +1259,11 @@ hstu_status_t hstu_cache_evict(const hstu_paged_cache_t* cache, int64_t num_seqs
   const size_t lb = (size_t)num_seqs * sizeof(int64_t);
   if (reinterpret_cast<uintptr_t>(new_lens) & 7) return HSTU_ERR_INVALID_ARG;
   if ((new_lens != cache_lens && overlaps(new_lens, lb, cache_lens, lb)) ||
-      overlaps(new_lens, lb, workspace, w.total) || overlaps_cache(new_lens, lb, *cache) ||
-      overlaps_cache(workspace, w.total, *cache) ||
-      !apart({{page_table, (size_t)(num_seqs * max_pages), 4}, {next_positions, (size_t)num_seqs, 8}}, *cache,
+      overlaps(new_lens, lb, workspace, w.total) || overlaps_cache(new_lens, lb, arrays) ||
+      overlaps_cache(workspace, w.total, arrays) ||
+      !apart({{page_table, (size_t)(num_seqs * max_pages), 4}, {next_positions, (size_t)num_seqs, 8}}, arrays,
              new_lens, lb, workspace, w.total) ||
-      !apart({{cache_lens, (size_t)num_seqs, 8}}, *cache, nullptr, 0, workspace, w.total))
+      !apart({{cache_lens, (size_t)num_seqs, 8}}, arrays, nullptr, 0, workspace, w.total))
     return HSTU_ERR_INVALID_ARG;
   paged::Evict a{};
   a.c = cache_view(*cache);
