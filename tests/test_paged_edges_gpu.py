@@ -221,3 +221,50 @@ def test_layer_behind_an_earlier_error(hstu):
         assert hstu.device_status() == hstu.HSTU_OK
         out.append(g["cache"].k.nan_to_num(7.0))
     assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
+
+
+@pytest.mark.parametrize("dtype,H,hd,ps,lens", [("bf16", 4, 64, 16, [900, 30, 2000, 500]), ("bf16", 8, 128, 64, [1300] * 9),
+                                                ("fp32", 3, 128, 16, [700, 701, 1]), ("bf16", 1, 64, 1024, [3000])])
+def test_calls_with_nothing_in_between(hstu, dtype, H, hd, ps, lens):
+    """Each kernel's launch overlaps the one before it, with no other kernel between them: a fill, scores that
+    sum weights, an eviction by them, more scores equal the same calls waited for one by one."""
+    B, grow = len(lens), 40
+    runs = []
+    for wait in (False, True):
+        c = Case(81, lens, H, hd, ps, dtype, extra=grow + 1)
+        g = c.on_device(hstu)
+        s = g["shape"]
+        g["shape"] = hstu.make_shape(B, B, max(lens) + grow + 2, s.d_model, H, hd, hd, s.dtype, s.n_pos_buckets,
+                                     s.n_time_buckets)
+        off = torch.arange(B + 1, device="cuda") * grow
+        rows = c.dev(values(c.rng, (B * grow, 4 * H * hd), dtype), c.torch_dtype())
+        ts = g["now"].repeat_interleave(grow)
+        more, seen = g["lens"] + grow, g["next"] + grow
+        ws = torch.empty(hstu.paged_attention_workspace_size(g["shape"]), dtype=torch.uint8, device="cuda")
+        es = torch.empty(hstu.cache_evict_workspace_size(g["cache"], B, c.M), dtype=torch.uint8, device="cuda")
+        av = [torch.empty_like(g["av"]) for _ in range(17)]
+        cut = torch.empty_like(more)
+        torch.cuda.synchronize()
+
+        def attend(k, lens, append=False):
+            hstu.hstu_paged_attention_fwd(g["shape"], g["cache"], g["uvqk"], g["table"], lens, seen, g["now"], g["pos"],
+                                          g["tim"], g["slopes"], c.scale, av[k], append=append, workspace=ws)
+        for repeat in range(4):
+            steps = [lambda: hstu.hstu_cache_append(g["cache"], rows, off, ts, g["table"], g["lens"], g["next"])]
+            steps += [lambda k=k: attend(4 * repeat + k, more, k == 2) for k in range(3)]
+            steps += [lambda: hstu.hstu_cache_evict(g["cache"], g["table"], more, seen, 600, 50, new_lens=cut, workspace=es),
+                      lambda: attend(4 * repeat + 3, cut, True)]
+            for step in steps:
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+        attend(16, more)
+        torch.cuda.synchronize()
+        assert hstu.device_status() == hstu.HSTU_OK
+        cache = g["cache"]
+        runs.append([*av, cut, cache.k, cache.v, cache.weights, cache.positions, cache.timestamps])
+    for a, b in zip(*runs):
+        if a.is_floating_point():
+            assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
+        else:
+            assert torch.equal(a, b)
